@@ -20,6 +20,7 @@ OK, EINVAL, ENOMEM, EHIP = 0, -1, -2, -3
 # name -> (restype, argtypes); mirrors include/adasum.h
 _VP = ctypes.c_void_p
 _I64P = ctypes.POINTER(ctypes.c_int64)
+_INT, _I64, _F64 = ctypes.c_int, ctypes.c_int64, ctypes.c_double
 SIGNATURES = {
     "adasum_combine": (ctypes.c_int, [_VP, ctypes.c_int, _I64P, ctypes.c_int, ctypes.c_int, _VP, _VP]),
     "adasum_workspace_bytes": (ctypes.c_int64, [ctypes.c_int, _I64P, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
@@ -30,6 +31,20 @@ SIGNATURES = {
     "adasum_sum": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_int64, ctypes.c_int, _VP, _VP, ctypes.c_size_t,
                                   _VP]),
     "adasum_sum_workspace_bytes": (ctypes.c_int64, [ctypes.c_int, ctypes.c_int64, ctypes.c_int]),
+    "adasum_embedding": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _INT, _I64, _F64, _VP, _I64, _INT, _VP]),
+    "adasum_embedding_grad_workspace_bytes": (_I64, [_I64, _I64, _INT]),
+    "adasum_embedding_grad": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _INT, _I64, _F64, _VP, _INT, _INT, _VP,
+                                     ctypes.c_size_t, _VP]),
+    "adasum_layer_norm": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _VP, _INT, _F64, _VP, _I64, _VP, _VP, _VP, _VP,
+                                 _VP]),
+    "adasum_layer_norm_grad_workspace_bytes": (_I64, [_I64, _I64, _INT]),
+    "adasum_layer_norm_grad": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _I64, _VP, _VP, _VP, _VP, _VP, _INT, _VP,
+                                      _I64, _VP, _VP, _INT, _INT, _VP, ctypes.c_size_t, _VP]),
+    "adasum_checkpoint_pack": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _VP, _VP]),
+    "adasum_checkpoint_unpack": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _INT, _VP]),
+    "adasum_linear_grad_workspace_bytes": (_I64, [_I64, _I64, _I64, _INT]),
+    "adasum_linear_grad": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _VP, _I64, _VP, _VP, _INT, _INT, _VP,
+                                  ctypes.c_size_t, _VP]),
     "adasum_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "adasum_last_error": (ctypes.c_char_p, []),
     "adasum_version": (ctypes.c_int, []),
@@ -76,8 +91,8 @@ def profile_begin():
 
 def profile_end():
     """Per-kernel-kind {launches, milliseconds, bytes} recorded since profile_begin()."""
-    rows = (KernelTime * 8)()
-    n = check(lib().adasum_profile_end(rows, 8))
+    rows = (KernelTime * 16)()
+    n = check(lib().adasum_profile_end(rows, 16))
     return {r.kernel.decode(): {"launches": r.launches, "milliseconds": r.milliseconds, "bytes": r.bytes}
             for r in rows[:n]}
 

@@ -210,8 +210,7 @@ std::map<std::pair<int, void*>, OwnedWorkspace> g_ws;  // (device, stream) -> bu
 
 // ---------------------------------------------------------------- launch timing
 
-enum KernelKind { kGram = 0, kTree, kWsum, kSum, kExact, kNumKinds };
-const char* const kKindNames[kNumKinds] = {"gram", "tree", "wsum", "sum", "exact"};
+const char* const kKindNames[kNumKinds] = {"gram", "tree", "wsum", "sum", "exact", "embedding", "norm", "pack", "linear"};
 
 struct ProfRecord {
   int kind;

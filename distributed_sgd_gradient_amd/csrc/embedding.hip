@@ -1,0 +1,560 @@
+// embedding.hip - rows of a table by token, and the table's gradient.
+//
+//   forward   y[i] = scale * table[t_i]
+//   backward  grad[t] = scale * (sum of dy[i] over the rows i with t_i = t),
+//             every row of grad written (or, accumulating, the named ones
+//             added to)
+//
+// A token outside [0, vocab) is no token: zeros forward, nothing backward.
+//
+// The gradient is a sum by token without atomics, in three launches:
+//   group   lists the rows of every token, in row order, the tokens dealt to
+//           the workgroups by their low bits; also clears the rows of grad
+//           that no token names
+//   sum     walks the grouped list in pieces of equal length, so that a
+//           frequent token is summed by many workgroups; a token whose rows
+//           lie inside one piece is written at once, the sums of the others
+//           are left for
+//   join    adds them in the order of the list, in fp64.
+// Every sum has a fixed order, so the result is bitwise reproducible.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "elem.h"
+#include "layer_ops.h"
+
+namespace adasum {
+namespace {
+
+using namespace elem;
+
+// ---------------------------------------------------------------- forward
+
+constexpr int kLookups = 4;  // pieces of 16 bytes of the table a lane has in flight
+
+template <typename T, typename O, typename TOK>
+__global__ __launch_bounds__(256) void embedding_kernel(EmbeddingArgs a) {
+  constexpr int VEC = Type<T>::kVec;
+  constexpr int N = VEC > Type<O>::kVec ? VEC : Type<O>::kVec;  // values per piece
+  const uint32_t per_row = (uint32_t)((a.hidden + N - 1) / N);
+  const int64_t total = a.n * per_row;
+  const TOK* tokens = static_cast<const TOK*>(a.tokens);
+  for (int64_t first = (int64_t)blockIdx.x * 256 * kLookups; first < total;
+       first += (int64_t)gridDim.x * 256 * kLookups) {
+    const int64_t row0 = first / per_row;
+    const uint32_t p0 = (uint32_t)(first - row0 * per_row);
+    int64_t row[kLookups], tok[kLookups];
+    int col[kLookups], valid[kLookups];
+#pragma unroll
+    for (int u = 0; u < kLookups; ++u) {
+      const uint32_t k = p0 + u * 256 + threadIdx.x;
+      const uint32_t q = k / per_row;
+      row[u] = row0 + q;
+      col[u] = (int)(k - q * per_row) * N;
+      valid[u] = row[u] < a.n ? a.hidden - col[u] : 0;
+      tok[u] = valid[u] > 0 ? (int64_t)tokens[row[u]] : -1;
+    }
+    float v[kLookups][N];
+#pragma unroll
+    for (int u = 0; u < kLookups; ++u) {
+      const bool there = tok[u] >= 0 && tok[u] < a.vocab;
+      load_row<T, N>(static_cast<const T*>(a.table) + (there ? tok[u] : 0) * a.table_stride + col[u],
+                     there ? valid[u] : 0, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kLookups; ++u) {
+      const bool there = tok[u] >= 0 && tok[u] < a.vocab;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[u][i] = there ? v[u][i] * a.scale : 0.f;
+      store_row<O, N>(static_cast<O*>(a.out) + row[u] * a.out_stride + col[u], v[u], valid[u]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- group
+
+constexpr int kGroupWaves = 16;
+constexpr int kGroupKeys = 512;  // most tokens a workgroup of the grouping kernel owns (32 KB of counts)
+constexpr int kGroupBatch = 4;   // steps of 256 tokens whose loads a wave has in flight
+
+// The tokens of four consecutive places from p on (i places into the list),
+// those past n or outside the vocabulary as -1.
+template <typename TOK>
+__device__ __forceinline__ void load_tokens(const TOK* tokens, int64_t i, int64_t n, int64_t vocab, int (&t)[4]) {
+  TOK raw[4];
+  if (i + 4 <= n) {
+    if constexpr (sizeof(TOK) == 4) {
+      const v4u r = load_at<v4u, 4>(tokens + i);
+      raw[0] = (TOK)r.x; raw[1] = (TOK)r.y; raw[2] = (TOK)r.z; raw[3] = (TOK)r.w;
+    } else {
+      typedef int64_t v2l __attribute__((ext_vector_type(2)));
+      const v2l r = load_at<v2l, 8>(tokens + i), s = load_at<v2l, 8>(tokens + i + 2);
+      raw[0] = r.x; raw[1] = r.y; raw[2] = s.x; raw[3] = s.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) raw[j] = i + j < n ? tokens[i + j] : (TOK)-1;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) t[j] = raw[j] >= 0 && (int64_t)raw[j] < vocab ? (int)raw[j] : -1;
+}
+
+struct GroupArgs {
+  const void* tokens;
+  int64_t n, vocab;
+  int shift;          // log2 of the number of workgroups
+  int keys;           // tokens per workgroup
+  int32_t* rows;      // grouped: row index
+  int32_t* grouped;   // grouped: token
+  int32_t* count;     // [1]: how many rows have a token
+  char* grad;         // cleared where no token names the row; NULL: nothing is cleared
+  int64_t row_bytes;
+};
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// Workgroup g owns the tokens t with t mod G = g (dealing them by their low
+// bits spreads the frequent ones, which many vocabularies put first).  Its 16
+// waves each scan a sixteenth of the list twice.  The first scan counts, per
+// wave, the rows of every owned token, and the rows of the tokens of lower
+// workgroups: their number is where this workgroup's part of the grouped list
+// begins, so the workgroups need nothing from each other.  The second scan
+// writes the owned rows; a wave's position for a token starts where the
+// counts of the waves before it end, so the rows of a token stay in order.
+template <typename TOK>
+__global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
+  extern __shared__ int32_t counts[];  // [16][keys]: counts, then positions
+  __shared__ int32_t lower[kGroupWaves], scan[kGroupWaves];
+  __shared__ int32_t totals[kGroupKeys];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int G = 1 << a.shift, g = blockIdx.x, keys = a.keys;
+  const TOK* tokens = static_cast<const TOK*>(a.tokens);
+  for (int i = tid; i < kGroupWaves * keys; i += 1024) counts[i] = 0;
+  __syncthreads();
+
+  const int64_t steps = (a.n + 1024 * 4 - 1) / (1024 * 4);  // of 256 tokens, per wave
+  const int64_t begin = wave * steps * 256;
+  const int mask = G - 1;
+  int32_t* mine = counts + wave * keys;
+  auto fetch = [&](int64_t s, int (&t)[kGroupBatch][4]) {
+#pragma unroll
+    for (int u = 0; u < kGroupBatch; ++u)
+      load_tokens(tokens, s + u < steps ? begin + (s + u) * 256 + lane * 4 : a.n, a.n, a.vocab, t[u]);
+  };
+
+  int less = 0;
+  for (int64_t s = 0; s < steps; s += kGroupBatch) {
+    int t[kGroupBatch][4];
+    fetch(s, t);
+#pragma unroll
+    for (int u = 0; u < kGroupBatch; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int low = t[u][j] >= 0 ? (t[u][j] & mask) : G;
+        less += low < g ? 1 : 0;
+        if (low == g) atomicAdd(&mine[t[u][j] >> a.shift], 1);
+      }
+  }
+  for (int o = 32; o > 0; o >>= 1) less += __shfl_xor(less, o);
+  if (lane == 0) lower[wave] = less;
+  __syncthreads();
+
+  // positions: the tokens in the order of their keys, each token's rows wave
+  // by wave (at most one key a thread)
+  int32_t total = 0;
+  if (tid < keys) {
+    for (int w = 0; w < kGroupWaves; ++w) total += counts[w * keys + tid];
+    totals[tid] = total;
+  }
+  int32_t before = total;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int32_t up = __shfl_up(before, o);
+    if (lane >= o) before += up;
+  }
+  if (lane == 63) scan[wave] = before;
+  __syncthreads();
+  int32_t base = 0, own = 0;
+  for (int w = 0; w < kGroupWaves; ++w) {
+    base += lower[w];
+    own += scan[w];
+    if (w < wave) before += scan[w];
+  }
+  if (g == G - 1 && tid == 0) *a.count = base + own;
+  if (tid < keys) {
+    int32_t at = base + before - total;
+    for (int w = 0; w < kGroupWaves; ++w) {
+      const int32_t c = counts[w * keys + tid];
+      counts[w * keys + tid] = at;
+      at += c;
+    }
+  }
+  // the gradient rows of owned tokens that the list does not hold
+  if (a.grad) {
+    for (int k = wave; k < keys; k += kGroupWaves) {
+      const int64_t t = ((int64_t)k << a.shift) + g;
+      if (t >= a.vocab || totals[k] != 0) continue;
+      char* row = a.grad + t * a.row_bytes;
+      const int64_t whole = a.row_bytes & ~int64_t(15);
+      for (int64_t i = lane * 16; i < whole; i += 1024) store_at<v4u, 1>(row + i, v4u{0u, 0u, 0u, 0u});
+      for (int64_t i = whole + lane * 2; i < a.row_bytes; i += 128) *reinterpret_cast<uint16_t*>(row + i) = 0;
+    }
+  }
+  __syncthreads();
+  if (own == 0) return;
+
+  for (int64_t s = 0; s < steps; s += kGroupBatch) {
+    int batch[kGroupBatch][4];
+    fetch(s, batch);
+#pragma unroll
+    for (int u = 0; u < kGroupBatch; ++u) {
+      const int64_t at = begin + (s + u) * 256 + lane * 4;
+      int(&t)[4] = batch[u];
+      uint64_t want[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) want[j] = __ballot(t[j] >= 0 && (t[j] & mask) == g);
+      // one token of this step after another: its rows' places are by lane,
+      // then by place in the lane
+      while (uint64_t left = want[0] | want[1] | want[2] | want[3]) {
+        const int src = __builtin_ctzll(left);
+        int pick = t[3];
+#pragma unroll
+        for (int j = 2; j >= 0; --j)
+          if ((want[j] >> lane) & 1u) pick = t[j];
+        const int token = __builtin_amdgcn_readlane(pick, src);
+        uint64_t eq[4];
+        int below = 0, sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          eq[j] = __ballot(((want[j] >> lane) & 1u) && t[j] == token);
+          want[j] &= ~eq[j];
+          below += lanes_below(eq[j]);
+          sum += __popcll(eq[j]);
+        }
+        const int key = token >> a.shift;
+        int pos = mine[key] + below;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((eq[j] >> lane) & 1u) {
+            a.rows[pos] = (int32_t)(at + j);
+            a.grouped[pos] = token;
+            ++pos;
+          }
+        // the wave's own counter: every lane has read it before lane 0 moves
+        // it on (the wave runs in step and its LDS operations stay in order);
+        // the fences keep the compiler from holding it in a register
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (lane == 0) mine[key] += sum;
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sum
+
+struct RunArgs {
+  const void* dy;
+  int64_t dy_stride;
+  int hidden, span, lanes_shift;
+  const int32_t* rows;
+  const int32_t* grouped;
+  const int32_t* count;
+  float scale;
+  void* grad;
+  int accumulate;
+  float* head;  // [workgroup][tiles * 64 * VEC]: the first run's sum where it began before the workgroup
+  float* tail;  // the last run's sum where it began in the workgroup and goes on after it
+  int64_t pitch;
+};
+
+constexpr int kSumThreads = 512;
+constexpr int kSumSpots = 2048;  // grouped positions of a workgroup at most
+constexpr int kSumBatch = 8;     // rows a lane has in flight
+
+template <typename O, int N>
+__device__ __forceinline__ void write_gradient(O* p, const float (&s)[N], float scale, int valid, bool accumulate) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = s[i] * scale;
+  if (accumulate) {
+    float old[N];
+    load_row<O, N>(p, valid, old);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += old[i];
+  }
+  store_row<O, N>(p, v, valid);
+}
+
+// A workgroup's `units` row groups of 2^lanes_shift lanes each walk `span`
+// consecutive grouped positions, one column vector a lane.  A run (the
+// positions of one token) belongs to the row group it begins in.  A row group
+// adds its part of a run begun before it into LDS (`heads`); the run's owner
+// collects these parts in order.  At the workgroup's ends the same is done
+// through memory by the join kernel.
+template <typename T, typename O>
+__global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
+  constexpr int VEC = Type<T>::kVec;
+  constexpr int N = VEC > Type<O>::kVec ? VEC : Type<O>::kVec;
+  __shared__ int32_t tok[kSumSpots + 2];  // tok[1 + i]: position i; tok[0], tok[spots + 1]: the neighbours
+  __shared__ int32_t row[kSumSpots];
+  __shared__ float heads[kSumThreads][N];
+  const int tid = threadIdx.x;
+  const int lanes = 1 << a.lanes_shift, units = kSumThreads >> a.lanes_shift;
+  const int unit = tid >> a.lanes_shift, lane = tid & (lanes - 1);
+  const int spots = units * a.span;
+  const int64_t first = (int64_t)blockIdx.x * spots;
+  const int64_t m = *a.count;
+  if (first >= m) return;
+  const int here = (int)(m - first < spots ? m - first : spots);
+  for (int i = tid; i < spots + 2; i += kSumThreads) {
+    const int64_t p = first + i - 1;
+    tok[i] = p >= 0 && p < m ? a.grouped[p] : -1;
+  }
+  for (int i = tid; i < here; i += kSumThreads) row[i] = a.rows[first + i];
+  __syncthreads();
+
+  const int col = (int)(blockIdx.y * lanes + lane) * N;
+  const int valid = a.hidden - col;
+  const T* dy = static_cast<const T*>(a.dy) + col;
+  O* grad = static_cast<O*>(a.grad) + col;
+  const int p0 = unit * a.span;
+  const int num = here - p0 < a.span ? (here - p0 > 0 ? here - p0 : 0) : a.span;
+
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  int token = num > 0 ? tok[1 + p0] : -1;
+  bool ours = num > 0 && tok[p0] != token;  // this run begins in this row group
+  bool head = false;                        // heads[tid] holds the end of a run begun before
+  for (int i0 = 0; i0 < num; i0 += kSumBatch) {
+    float v[kSumBatch][N];
+    // no branch around the loads: positions past the last read row 0 of the
+    // batch again and are dropped
+#pragma unroll
+    for (int u = 0; u < kSumBatch; ++u) {
+      const int i = i0 + u < num ? i0 + u : i0;
+      load_row<T, N>(dy + (int64_t)row[p0 + i] * a.dy_stride, valid, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kSumBatch; ++u) {
+      if (i0 + u >= num) continue;
+      const int t = tok[1 + p0 + i0 + u];
+      if (t != token) {
+        if (ours) {
+          write_gradient<O, N>(grad + (int64_t)token * a.hidden, acc, a.scale, valid, a.accumulate);
+        } else {
+          head = true;
+#pragma unroll
+          for (int i = 0; i < N; ++i) heads[tid][i] = acc[i];
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.f;
+        token = t;
+        ours = true;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += v[u][i];
+    }
+  }
+  if (num > 0 && !ours) {
+    // the whole row group lies in a run begun before it
+    head = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) heads[tid][i] = acc[i];
+  }
+  __syncthreads();
+  if (num == 0) return;
+  // collect the parts of later row groups: of this row group's last run, and
+  // in row group 0 also of a run begun before the workgroup
+  const int64_t spot = (int64_t)blockIdx.x * a.pitch + col;
+  auto collect = [&](float (&sum)[N], int t) {
+    int u = unit + 1;
+    for (; u < units && tok[1 + u * a.span] == t && u * a.span < here; ++u) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum[i] += heads[u * lanes + lane][i];
+      // the run ends inside row group u unless its last position has the token
+      const int last = min((u + 1) * a.span, here);
+      if (tok[last] != t) return false;
+    }
+    return true;  // not seen to end inside the workgroup's positions
+  };
+  if (unit == 0 && head) {
+    const int t = tok[1];
+    const int last = min(a.span, here);
+    float sum[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = heads[tid][i];
+    if (tok[last] == t) (void)collect(sum, t);
+    if (valid > 0) store_row<float, N>(a.head + spot, sum, N);
+  }
+  if (ours) {
+    const bool on = collect(acc, token) && tok[here + 1] == token;
+    if (on) {
+      if (valid > 0) store_row<float, N>(a.tail + spot, acc, N);
+    } else {
+      write_gradient<O, N>(grad + (int64_t)token * a.hidden, acc, a.scale, valid, a.accumulate);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join
+
+// A run that begins in workgroup b's positions and goes on after them: its
+// tail and the heads of the workgroups it reaches, in order, one column a
+// thread.
+__global__ __launch_bounds__(256) void join_runs_kernel(RunArgs a, int spots, int grad_dtype) {
+  const int64_t m = *a.count;
+  const int64_t first = (int64_t)blockIdx.x * spots, next = first + spots;
+  if (next >= m) return;
+  const int32_t t = a.grouped[next - 1];
+  if (a.grouped[next] != t) return;
+  // the run's owner is this workgroup unless all its positions belong to a
+  // run begun before it
+  if (first > 0 && a.grouped[first] == t && a.grouped[first - 1] == t) return;
+  // workgroups whose first position has the token, found 64 at a time
+  int64_t reach = 0;
+  const int64_t blocks = (m + spots - 1) / spots;
+  for (;;) {
+    const int64_t b = blockIdx.x + 1 + reach + (threadIdx.x & 63);
+    const uint64_t off = ~__ballot(b < blocks && a.grouped[b * spots] == t);
+    if (off != 0) {
+      reach += __builtin_ctzll(off);
+      break;
+    }
+    reach += 64;
+  }
+  const int64_t col = (int64_t)blockIdx.y * 256 + threadIdx.x;
+  if (col >= a.hidden) return;
+  double s = (double)a.tail[blockIdx.x * a.pitch + col];
+  const float* head = a.head + ((int64_t)blockIdx.x + 1) * a.pitch + col;
+#pragma unroll 16
+  for (int64_t b = 0; b < reach; ++b) s += (double)head[b * a.pitch];
+  s *= (double)a.scale;
+  const int64_t i = (int64_t)t * a.hidden + col;
+  store_any(a.grad, grad_dtype, i, a.accumulate ? s + (double)load_any(a.grad, grad_dtype, i) : s);
+}
+
+size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+
+int group_shift(int64_t vocab) {
+  // one workgroup per CU, more where a workgroup would own too many tokens,
+  // fewer where there are fewer tokens
+  int shift = 8;
+  while (shift > 0 && (int64_t(1) << (shift - 1)) >= vocab) --shift;
+  while (ceil_div(vocab, int64_t(1) << shift) > kGroupKeys) ++shift;
+  return shift;
+}
+
+}  // namespace
+
+hipError_t launch_embedding(int table_dtype, int out_dtype, const EmbeddingArgs& a, hipStream_t st) {
+  return with_dtype(table_dtype, [&](auto t) {
+    return with_dtype(out_dtype, [&](auto o) {
+      using T = decltype(t);
+      using O = decltype(o);
+      constexpr int N = Type<T>::kVec > Type<O>::kVec ? Type<T>::kVec : Type<O>::kVec;
+      const int64_t pieces = a.n * ceil_div(a.hidden, N);
+      const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(pieces, 256 * kLookups), int64_t(1) << 20);
+      if (a.token_bytes == 4)
+        embedding_kernel<T, O, int32_t><<<blocks, 256, 0, st>>>(a);
+      else
+        embedding_kernel<T, O, int64_t><<<blocks, 256, 0, st>>>(a);
+      return hipGetLastError();
+    });
+  });
+}
+
+EmbeddingGradLayout embedding_grad_layout(int64_t n, int hidden, int dtype) {
+  EmbeddingGradLayout l{};
+  // 8 columns a lane where either side is 16 bits wide; the layout does not
+  // depend on the gradient's type, so it takes the narrower vector
+  const int vec = dtype == 0 ? 4 : 8;
+  l.lanes = 1;
+  while (l.lanes < 64 && l.lanes * vec < hidden) l.lanes *= 2;
+  l.units = kSumThreads / l.lanes;
+  l.tiles = (int)ceil_div(hidden, (int64_t)l.lanes * vec);
+  // long spans leave less to join, short ones fill the GPU: the longest of 8
+  // to 32 positions with two workgroups per CU
+  l.span = 32;
+  while (l.span > 8 && ceil_div(n, (int64_t)l.units * l.span) * l.tiles < 2 * kCUs) l.span /= 2;
+  while (l.span > 1 && l.units * l.span > kSumSpots) l.span /= 2;
+  l.blocks = ceil_div(n, (int64_t)l.units * l.span);
+  const size_t pitch = (size_t)l.tiles * l.lanes * 8;
+  size_t at = 0;
+  l.rows = at;
+  at += align256((size_t)n * 4);
+  l.tokens = at;
+  at += align256((size_t)n * 4);
+  l.count = at;
+  at += 256;
+  l.head = at;
+  at += align256((size_t)l.blocks * pitch * 4);
+  l.tail = at;
+  at += align256((size_t)l.blocks * pitch * 4);
+  l.total = at;
+  return l;
+}
+
+hipError_t launch_embedding_grad(int dtype, const EmbeddingGradArgs& a, hipStream_t st) {
+  const EmbeddingGradLayout l = embedding_grad_layout(a.n, a.hidden, dtype);
+  const int grad_size = a.grad_dtype == 0 ? 4 : 2;
+  GroupArgs g{};
+  g.tokens = a.tokens;
+  g.n = a.n;
+  g.vocab = a.vocab;
+  g.shift = group_shift(a.vocab);
+  g.keys = (int)ceil_div(a.vocab, int64_t(1) << g.shift);
+  g.rows = reinterpret_cast<int32_t*>(a.ws + l.rows);
+  g.grouped = reinterpret_cast<int32_t*>(a.ws + l.tokens);
+  g.count = reinterpret_cast<int32_t*>(a.ws + l.count);
+  g.grad = a.accumulate ? nullptr : static_cast<char*>(a.grad);
+  g.row_bytes = (int64_t)a.hidden * grad_size;
+  const size_t lds = (size_t)kGroupWaves * g.keys * sizeof(int32_t);
+  const unsigned groups = 1u << g.shift;
+  if (a.token_bytes == 4)
+    group_kernel<int32_t><<<groups, 1024, lds, st>>>(g);
+  else
+    group_kernel<int64_t><<<groups, 1024, lds, st>>>(g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.n == 0) return e;
+
+  RunArgs s{};
+  s.dy = a.dy;
+  s.dy_stride = a.dy_stride;
+  s.hidden = a.hidden;
+  s.span = l.span;
+  while ((1 << s.lanes_shift) < l.lanes) ++s.lanes_shift;
+  s.rows = g.rows;
+  s.grouped = g.grouped;
+  s.count = g.count;
+  s.scale = a.scale;
+  s.grad = a.grad;
+  s.accumulate = a.accumulate;
+  s.head = reinterpret_cast<float*>(a.ws + l.head);
+  s.tail = reinterpret_cast<float*>(a.ws + l.tail);
+  s.pitch = (int64_t)l.tiles * l.lanes * 8;
+  e = with_dtype(dtype, [&](auto t) {
+    return with_dtype(a.grad_dtype, [&](auto o) {
+      using T = decltype(t);
+      using O = decltype(o);
+      constexpr int N = Type<T>::kVec > Type<O>::kVec ? Type<T>::kVec : Type<O>::kVec;
+      const unsigned tiles = (unsigned)ceil_div(a.hidden, (int64_t)l.lanes * N);
+      sum_runs_kernel<T, O><<<dim3((unsigned)l.blocks, tiles), kSumThreads, 0, st>>>(s);
+      return hipGetLastError();
+    });
+  });
+  if (e != hipSuccess) return e;
+  if (l.blocks > 1) {
+    join_runs_kernel<<<dim3((unsigned)(l.blocks - 1), (unsigned)ceil_div(a.hidden, 256)), 256, 0, st>>>(
+        s, l.units * l.span, a.grad_dtype);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace adasum

@@ -1,6 +1,8 @@
 // library.h - internal interface between the library's host sources: the
 // plan cache, argument validation and the stage scheduler (adasum.hip), used
-// by the entry point that works in a fixed scratch array (noalloc.hip).
+// by the entry point that works in a fixed scratch array (noalloc.hip); its
+// errors, pointer checks and launch timing also by the layer operators'
+// entry points (layer_ops.hip).
 // Nothing here is exported from the shared library.
 #pragma once
 
@@ -67,6 +69,19 @@ int validate_buffers(const void* const* grads, int K, int64_t N, size_t esz, int
 int check_devices(const void* const* grads, int K, size_t vec_bytes, const void* out, const void* ws,
                   size_t ws_needed, const double* coeffs, const double* stats, const double* ortho, size_t nodes,
                   int nseg, int device);
+
+// p is device memory of `device`, with `bytes` bytes from it inside its
+// allocation where the runtime knows that allocation's extent.
+int check_device_range(const void* p, size_t bytes, const char* name, int device);
+
+// ADASUM_LOG is set: launches are traced on stderr.
+bool log_enabled();
+
+// Launch timing (adasum_profile_begin): the events around one record.  Caller
+// holds g_mu.
+enum KernelKind { kGram = 0, kTree, kWsum, kSum, kExact, kEmbedding, kNorm, kPack, kLinear, kNumKinds };
+int prof_start(int kind, double bytes, hipStream_t st);
+void prof_stop(int idx, hipStream_t st);
 
 // Whether work enqueued on st now is being captured into a graph.
 bool capturing(hipStream_t st);

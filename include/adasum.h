@@ -205,10 +205,156 @@ ADASUM_API int adasum_sum(const void* const* grads, int K, int64_t N, int dtype,
                           size_t workspace_bytes, void* stream);
 ADASUM_API int64_t adasum_sum_workspace_bytes(int K, int64_t N, int dtype);
 
+/* ------------------------------------------------------------------------
+ * Layer operators: what a worker computes from its own microbatch before its
+ * gradient is combined with the others'.  Their gradients are written where
+ * the combine reads them: dweight, dbias and grad may be segments of a flat
+ * gradient buffer.
+ *
+ * Conventions, besides those above
+ *   - A matrix is rows x columns, its rows `stride` elements apart (at least
+ *     the number of columns), the elements of a row consecutive.  Without a
+ *     stride argument it is dense.
+ *   - Data pointers need only the alignment of their element type; the
+ *     workspace 16 bytes.  Buffers that are written may overlap no other
+ *     argument, where a matrix takes everything from its first to its last
+ *     element.
+ *   - dtype, param_dtype, grad_dtype, ... are adasum_dtype_t.  Arithmetic is
+ *     fp32, results are rounded once to nearest even; sums over rows are fp32
+ *     in pieces of bounded length, joined in fp64.
+ *   - accumulate != 0 adds the gradient to what dweight, dbias or grad holds
+ *     (the microbatches of one step) instead of replacing it.
+ *   - Zero rows (or tokens) are allowed: gradients are then zero (unchanged
+ *     when accumulating), other outputs empty.  Widths and vocab are >= 1.
+ *   - A call allocates, copies and synchronises nothing: it may be captured
+ *     into a HIP graph from the first one on.  Its workspace belongs to the
+ *     calls that use it: calls that share one must be ordered on one stream
+ *     (and graphs that share one must not run at the same time).
+ *   - Errors: ADASUM_EINVAL (NULL, size, stride, dtype, alignment, overlap,
+ *     workspace too small, not device memory of the current device),
+ *     ADASUM_EHIP.
+ */
+
+/*
+ * adasum_embedding - rows of a table by token:
+ * out[i] = scale * table[tokens[i]], and zeros where tokens[i] is outside
+ * [0, vocab): such a token is no token (padding, or a row that another
+ * worker's part of the table holds).
+ *
+ *   table        vocab rows of hidden elements of table_dtype, vocab <= 2^24.
+ *   tokens       n indices of token_bytes (4 or 8: int32 or int64) each.
+ *   scale        finite in fp32.
+ *   out          n rows of hidden elements of out_dtype.
+ */
+ADASUM_API int adasum_embedding(const void* table, int64_t vocab, int64_t hidden, int64_t table_stride,
+                                int table_dtype, const void* tokens, int token_bytes, int64_t n, double scale,
+                                void* out, int64_t out_stride, int out_dtype, void* stream);
+
+/*
+ * adasum_embedding_grad - the table's gradient:
+ * grad[t] = scale * (sum of dy[i] over the rows i with tokens[i] = t), for
+ * every t in [0, vocab): rows that no token names are zero (unchanged when
+ * accumulating).  Rows of dy whose token is none are not read.  The rows of a
+ * token are summed in a fixed order, without atomics on the sums.
+ *
+ *   dy           n rows of hidden elements of dtype.
+ *   grad         dense, vocab x hidden elements of grad_dtype.
+ *   workspace    adasum_embedding_grad_workspace_bytes(n, hidden, dtype) bytes.
+ */
+ADASUM_API int64_t adasum_embedding_grad_workspace_bytes(int64_t n, int64_t hidden, int dtype);
+ADASUM_API int adasum_embedding_grad(const void* dy, int64_t n, int64_t hidden, int64_t dy_stride, int dtype,
+                                     const void* tokens, int token_bytes, int64_t vocab, double scale, void* grad,
+                                     int grad_dtype, int accumulate, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * adasum_layer_norm - y = (x - mean) * rstd * weight + bias for every row,
+ * with mean the row's mean and rstd = 1 / sqrt(variance + eps).
+ *
+ *   x, y         rows x hidden elements of dtype, hidden <= 16384.
+ *   weight, bias hidden elements of param_dtype each; NULL: 1 and 0.
+ *   eps          a positive normal fp32 number.
+ *   mean, rstd   rows fp32 values each, for the backward pass; mean may be
+ *                NULL.
+ *   codes, scales
+ *                NULL, or where the normalised rows (x - mean) * rstd are
+ *                kept in 8 bits for the backward pass (the format of
+ *                adasum_checkpoint_pack): the backward pass then needs
+ *                neither x nor mean.
+ */
+ADASUM_API int adasum_layer_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, int dtype,
+                                 const void* weight, const void* bias, int param_dtype, double eps, void* y,
+                                 int64_t y_stride, float* mean, float* rstd, int8_t* codes, uint8_t* scales,
+                                 void* stream);
+
+/*
+ * adasum_layer_norm_grad - the backward pass.  With g = dy * weight and n the
+ * normalised rows:
+ *   dx      = rstd * (g - mean(g) - n * mean(g * n)), means over a row;
+ *   dweight = sum over rows of dy * n;   dbias = sum over rows of dy.
+ *
+ *   x, mean      the forward pass's; or both NULL and
+ *   codes, scales the normalised rows kept by the forward pass.
+ *   dx           rows x hidden elements of dtype (that of dy and x).
+ *   dweight, dbias
+ *                hidden elements of grad_dtype each; NULL: not wanted.
+ *   workspace    adasum_layer_norm_grad_workspace_bytes(...) bytes; may be
+ *                NULL where neither dweight nor dbias is wanted.
+ */
+ADASUM_API int64_t adasum_layer_norm_grad_workspace_bytes(int64_t rows, int64_t hidden, int dtype);
+ADASUM_API int adasum_layer_norm_grad(const void* dy, int64_t rows, int64_t hidden, int64_t dy_stride, int dtype,
+                                      const void* x, int64_t x_stride, const float* mean, const int8_t* codes,
+                                      const uint8_t* scales, const float* rstd, const void* weight, int param_dtype,
+                                      void* dx, int64_t dx_stride, void* dweight, void* dbias, int grad_dtype,
+                                      int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * adasum_checkpoint_pack - activations in 8 bits for the backward pass;
+ * adasum_checkpoint_unpack reads them back.
+ *
+ * 32 consecutive values of a row (fewer at its end) share a power of two:
+ * value = codes[r][c] * 2^(scales[r][c / 32] - 127), codes in [-127, 127].
+ * The power is the least with 127 steps reaching the block's largest
+ * magnitude, and codes are rounded to nearest even, so a value is off by at
+ * most half a step, 1/127 of the block's largest magnitude.  Steps are at
+ * least 2^-127, and at most 2^121 (2^9 for fp16), so that no value rounds up
+ * to an infinity.  A block that holds an infinity or NaN has scale 255 and
+ * reads back as NaNs.
+ *
+ *   x, out       rows x hidden elements of dtype.
+ *   codes        dense, rows x hidden.
+ *   scales       dense, rows x ceil(hidden / 32).
+ */
+ADASUM_API int adasum_checkpoint_pack(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, int dtype,
+                                      int8_t* codes, uint8_t* scales, void* stream);
+ADASUM_API int adasum_checkpoint_unpack(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t hidden,
+                                        void* out, int64_t out_stride, int dtype, void* stream);
+
+/*
+ * adasum_linear_grad - the gradient of y = x weight^T + bias from activations
+ * kept in 8 bits: dweight[o][i] = sum over rows of dy[r][o] * x[r][i],
+ * dbias[o] = sum over rows of dy[r][o].  Products are exact.
+ *
+ *   dy           rows x out_features elements of dtype.
+ *   codes, scales rows x in_features activations packed from dtype (fp16:
+ *                their values must be fp16 values, as packed ones are).
+ *   dweight      dense, out_features x in_features elements of grad_dtype.
+ *   dbias        out_features elements of grad_dtype; NULL: not wanted.
+ *   workspace    adasum_linear_grad_workspace_bytes(...) bytes (0 for few
+ *                rows, then NULL is allowed).
+ */
+ADASUM_API int64_t adasum_linear_grad_workspace_bytes(int64_t rows, int64_t out_features, int64_t in_features,
+                                                      int dtype);
+ADASUM_API int adasum_linear_grad(const void* dy, int64_t rows, int64_t out_features, int64_t dy_stride, int dtype,
+                                  const int8_t* codes, const uint8_t* scales, int64_t in_features, void* dweight,
+                                  void* dbias, int grad_dtype, int accumulate, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /*
  * Kernel timing, for benchmarks.  Between adasum_profile_begin() and
  * adasum_profile_end(), every kernel launch that any combine call of this
- * process enqueues is bracketed by a pair of HIP events recorded on that
+ * process enqueues (and the launches of every layer operator's call, as one)
+ * is bracketed by a pair of HIP events recorded on that
  * call's stream.  adasum_profile_end() waits for those events, disables the
  * recording, and writes one row per kernel kind: the launch count, the summed
  * launch durations and the summed algorithmic bytes (every operand read
@@ -217,7 +363,9 @@ ADASUM_API int64_t adasum_sum_workspace_bytes(int K, int64_t N, int dtype);
  */
 typedef struct {
   char kernel[32];     /* "gram", "tree", "exact", "wsum" (a small combine's
-                          fused walk and weighted sum counts here), "sum" */
+                          fused walk and weighted sum counts here), "sum";
+                          of the layer operators "embedding", "norm", "pack"
+                          and "linear", one count and one duration a call */
   int launches;
   double milliseconds;
   double bytes;

@@ -1,0 +1,887 @@
+"""Layer operators on the GPU against their formulas in 64 bits.
+
+Tolerances are counted in roundings.  U[dtype] is half a step, the largest
+relative error of one rounding; fp32 arithmetic contributes E = 2^-24 per
+rounding, and a sum of terms t_i whose longest chain of additions is d is off
+by at most d * E * sum |t_i|.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import distributed_sgd_gradient_amd as A
+import oracle
+from conftest import flush_print
+from distributed_sgd_gradient_amd import _native
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+DTYPES = [F32, F16, BF16]
+E = 2.0 ** -24
+U = {t: torch.finfo(t).eps / 2 for t in DTYPES}
+# half a step of the subnormals
+TINY = {t: torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2 for t in DTYPES}
+ids = lambda v: str(v).replace("torch.", "")  # noqa: E731
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def randn(seed, *shape, dtype=F32, std=1.0, mean=0.0):
+    """Normal values on the GPU, made on the host from the seed."""
+    return (torch.randn(*shape, generator=gen(seed), dtype=torch.float64) * std + mean).to(dtype).cuda()
+
+
+def within(got, want, bound, what):
+    """|got - want| <= bound everywhere, NaN where and only where want is."""
+    got, want = got.double().cpu(), want.double().cpu()
+    bound = torch.as_tensor(bound, dtype=torch.float64).cpu().expand_as(want)
+    assert got.shape == want.shape, (got.shape, want.shape)
+    nan = want.isnan()
+    assert torch.equal(got.isnan(), nan), f"{what}: NaNs differ"
+    inf = want.isinf() & ~nan
+    assert torch.equal(got[inf], want[inf]), f"{what}: infinities differ"
+    ok = ~(nan | inf)
+    err = (got - want).abs()[ok]
+    lim = bound[ok]
+    if err.numel():
+        worst = float((err / lim.clamp(min=1e-300)).max())
+        flush_print(f"  {what}: worst error {worst:.3f} of its bound")
+        assert worst <= 1.0, f"{what}: {worst} of the bound"
+
+
+def unaligned(t, skip=1):
+    """The same values in memory that starts `skip` elements into its allocation."""
+    flat = torch.empty(t.numel() + skip + 8, dtype=t.dtype, device=t.device)
+    v = flat[skip:skip + t.numel()].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+def strided(t, gap=5):
+    """The same rows, `gap` elements apart; the gaps hold NaN."""
+    wide = torch.full((t.size(0), t.size(1) + gap), float("nan"), dtype=t.dtype, device=t.device)
+    wide[:, 2:2 + t.size(1)] = t
+    return wide[:, 2:2 + t.size(1)]
+
+
+# ---------------------------------------------------------------- embedding
+
+
+def tokens_of(seed, n, vocab, kind):
+    g = gen(seed)
+    t = torch.randint(0, vocab, (n,), generator=g)
+    if kind == "frequent":  # half the rows one token
+        t[torch.rand(n, generator=g) < 0.5] = vocab // 2
+    elif kind == "one":
+        t[:] = vocab - 1
+    elif kind == "none":
+        t[:] = -1
+    elif kind == "outside":
+        r = torch.rand(n, generator=g)
+        t[r < 0.2] = -1
+        t[(r >= 0.2) & (r < 0.4)] = vocab
+        t[(r >= 0.4) & (r < 0.45)] = 2 ** 31 - 1
+        t[(r >= 0.45) & (r < 0.5)] = -2 ** 31
+    return t.cuda()
+
+
+def plain_embedding(table, tokens, scale):
+    v = table.size(0)
+    ok = (tokens >= 0) & (tokens < v)
+    rows = table.double()[tokens.clamp(0, v - 1)] * scale
+    return torch.where(ok[..., None], rows, torch.zeros_like(rows))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("n,vocab,hidden", [(1, 1, 1), (1, 30522, 768), (3, 2, 7), (129, 50, 8), (1000, 513, 33),
+                                            (77, 1000, 1001), (4096, 300, 64), (2, 5, 5000)])
+def test_embedding(gpu, n, vocab, hidden, dtype):
+    flush_print(f"embedding n={n} vocab={vocab} hidden={hidden} {dtype}")
+    scale = math.sqrt(hidden)
+    s32 = float(np.float32(scale))
+    table = randn(1, vocab, hidden, dtype=dtype)
+    for kind in ("uniform", "outside"):
+        t = tokens_of(2, n, vocab, kind)
+        for tok in (t, t.to(torch.int32)):
+            for out in DTYPES:
+                y = A.embedding(table, tok, scale=scale, dtype=out)
+                want = plain_embedding(table, t, s32)
+                # one product in fp32, one rounding to the output type
+                within(y, want, want.abs() * (E + U[out]) * 1.0001 + TINY[out], f"{kind} {out}")
+
+
+def test_embedding_strides_and_shapes(gpu):
+    table = strided(randn(3, 100, 37, dtype=BF16))
+    t = tokens_of(4, 24, 100, "outside").view(2, 3, 4)
+    base = A.embedding(table.contiguous(), t.contiguous())
+    assert base.shape == (2, 3, 4, 37)
+    assert torch.equal(A.embedding(table, t), base)
+    assert torch.equal(A.embedding(unaligned(table.contiguous(), 3), t), base)
+    out = strided(torch.zeros(24, 37, dtype=BF16, device="cuda"))
+    A.embedding(table, t.view(-1), out=out)
+    assert torch.equal(out, base.view(24, 37))
+    assert bool(out._base[:, :2].isnan().all()) and bool(out._base[:, 39:].isnan().all())
+    big = t.to(torch.int64) + (t == 3).to(torch.int64) * (1 << 40)  # a 64-bit token whose low half is a valid one
+    want = plain_embedding(table, big, 1.0)
+    assert torch.equal(A.embedding(table, big).double(), want)
+
+
+def plain_embedding_grad(dy, tokens, vocab, scale):
+    g = torch.zeros(vocab + 1, dy.size(-1), dtype=torch.float64)
+    t = tokens.cpu().view(-1)
+    t = torch.where((t < 0) | (t >= vocab), torch.full_like(t, vocab), t)
+    d = dy.double().cpu().reshape(-1, dy.size(-1))
+    d = torch.where((t == vocab)[:, None], torch.zeros_like(d), d)
+    g.index_add_(0, t, d)
+    a = torch.zeros_like(g)
+    a.index_add_(0, t, d.abs())
+    return g[:vocab] * scale, a[:vocab] * abs(scale)
+
+
+@pytest.mark.parametrize("kind", ["uniform", "frequent", "one", "none", "outside"])
+@pytest.mark.parametrize("n,vocab,hidden", [(1, 1, 1), (5, 3, 4), (64, 2, 8), (300, 17, 40), (1023, 700, 129),
+                                            (5000, 2, 64), (4097, 1, 1001), (2500, 3001, 3), (20000, 40, 24),
+                                            (9000, 140000, 8)])
+def test_embedding_grad(gpu, n, vocab, hidden, kind):
+    flush_print(f"embedding_grad n={n} vocab={vocab} hidden={hidden} {kind}")
+    t = tokens_of(7, n, vocab, kind)
+    for dtype in DTYPES:
+        dy = randn(8, n, hidden, dtype=dtype)
+        ref, mag = plain_embedding_grad(dy, t, vocab, 0.75)
+        for out in (F32, dtype):
+            for tok in (t, t.to(torch.int32)):
+                got = A.embedding_grad(dy, tok, vocab, scale=0.75, dtype=out)
+                # chains: at most 32 rows of a row group, 512 row groups of a
+                # workgroup, then fp64; one product by the scale
+                within(got, ref, (ref.abs() * (2 * E + U[out]) + mag * min(n, 544) * E) * 1.001 + TINY[out],
+                       f"{dtype} -> {out}")
+
+
+def test_embedding_grad_masked_rows_are_not_read(gpu):
+    n, vocab, hidden = 777, 60, 50
+    t = tokens_of(9, n, vocab, "outside")
+    dy = randn(10, n, hidden)
+    ref = A.embedding_grad(dy, t, vocab)
+    bad = (t < 0) | (t >= vocab)
+    dy2 = torch.where(bad[:, None], torch.full_like(dy, float("nan")), dy)
+    assert torch.equal(A.embedding_grad(dy2, t, vocab), ref)
+    # NaN and infinity of a row stay in its token's row of the gradient
+    dy2[(t == 7).nonzero()[0, 0]] = float("inf")
+    got = A.embedding_grad(dy2, t, vocab)
+    keep = torch.arange(vocab, device="cuda") != 7
+    assert torch.equal(got[keep], ref[keep]) and bool(got[7].isinf().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_embedding_grad_into_a_segment(gpu, dtype):
+    """Written into and added to a segment that starts at any element, and
+    nothing around it touched."""
+    n, vocab, hidden = 600, 41, 33
+    t = tokens_of(11, n, vocab, "frequent")
+    t[t == 3] = 4  # a token that no row has
+    dy = strided(randn(12, n, hidden, dtype=dtype))
+    ref, mag = plain_embedding_grad(dy, t, vocab, 1.0)
+    flat = torch.full((vocab * hidden + 20,), 2.5, dtype=dtype, device="cuda")
+    seg = flat[7:7 + vocab * hidden]
+    got = A.embedding_grad(dy, t, vocab, out=seg)
+    assert got.data_ptr() == seg.data_ptr()
+    bound = ref.abs() * (2 * E + U[dtype]) + mag * 544 * E + TINY[dtype]
+    within(seg.view(vocab, hidden), ref, bound, "written")
+    first = seg.clone().view(vocab, hidden)
+    assert bool((first[3] == 0).all())
+    A.embedding_grad(dy, t, vocab, out=seg, accumulate=True)
+    want = first.double().cpu() + ref
+    within(seg.view(vocab, hidden), want, want.abs() * (U[dtype] + 2 * E) + mag * 545 * E + TINY[dtype], "added")
+    assert torch.equal(seg.view(vocab, hidden)[3], first[3])
+    assert bool((flat[:7] == 2.5).all()) and bool((flat[7 + vocab * hidden:] == 2.5).all())
+
+
+def test_no_rows(gpu):
+    none = torch.zeros(0, dtype=torch.int64, device="cuda")
+    dy = torch.zeros(0, 12, device="cuda")
+    assert A.embedding(torch.ones(3, 12, device="cuda"), none).shape == (0, 12)
+    assert bool((A.embedding_grad(dy, none, 5) == 0).all())
+    g = torch.ones(5, 12, device="cuda")
+    A.embedding_grad(dy, none, 5, out=g, accumulate=True)
+    assert bool((g == 1).all())
+    w = torch.ones(12, device="cuda")
+    y, mean, rstd = A.layer_norm(dy, w, w)
+    assert y.shape == (0, 12) and mean.shape == (0,)
+    dx, dw, db = A.layer_norm_grad(dy, dy, mean, rstd, w)
+    assert dx.shape == (0, 12) and bool((dw == 0).all()) and bool((db == 0).all())
+    codes, scales = A.checkpoint_pack(dy)
+    assert codes.shape == (0, 12) and scales.shape == (0, 1)
+    assert A.checkpoint_unpack(codes, scales).shape == (0, 12)
+    dw, db = A.linear_grad(torch.zeros(0, 9, device="cuda"), codes, scales)
+    assert dw.shape == (9, 12) and bool((dw == 0).all()) and bool((db == 0).all())
+
+
+# ---------------------------------------------------------------- layer norm
+
+WIDTHS = [1, 2, 7, 8, 31, 33, 64, 100, 511, 512, 513, 768, 1001, 1024, 1025, 2048, 2047, 4096, 4097, 8193, 16384]
+
+
+def plain_norm(x, weight, bias, eps):
+    x = x.double()
+    mean = x.mean(-1, keepdim=True)
+    rstd = 1 / torch.sqrt((x - mean).square().mean(-1, keepdim=True) + eps)
+    n = (x - mean) * rstd
+    y = n if weight is None else n * weight.double()
+    return (y if bias is None else y + bias.double()), mean[..., 0], rstd[..., 0], n
+
+
+# A row's mean is summed over at most 16 values of a lane, 6 steps across a
+# wave and 16 waves: 38 additions.  Deviations are taken from the rounded mean
+# and what it lacks is taken out again, so the mean costs 38 E of the mean
+# deviation (<= 1 / rstd); the variance 38 E, half of that in rstd, and 3 for
+# the root; the rest are single roundings.
+N_ERR = 40 * E
+
+
+def norm_bounds(y, n, weight, bias, dtype):
+    w = 1.0 if weight is None else weight.double().abs()
+    b = 0.0 if bias is None else bias.double().abs()
+    dn = N_ERR * (n.abs() + 1)
+    return w * dn + 2 * E * (w * n.abs() + b) + U[dtype] * y.abs() + TINY[dtype], dn
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("hidden", WIDTHS)
+def test_layer_norm(gpu, hidden, dtype):
+    for rows in (1, 5, 37):
+        x = randn(20, rows, hidden, dtype=dtype, mean=0.5)
+        w, b = randn(21, hidden, mean=1.0, std=0.2), randn(22, hidden)
+        flush_print(f"layer_norm rows={rows} hidden={hidden} {dtype}")
+        y, mean, rstd = A.layer_norm(x, w, b, eps=1e-6)
+        ry, rm, rr, n = plain_norm(x, w, b, 1e-6)
+        bound, _ = norm_bounds(ry, n, w, b, dtype)
+        within(y, ry, bound, "y")
+        within(mean, rm, E * rm.abs() + N_ERR / rr, "mean")
+        within(rstd, rr, N_ERR * rr, "rstd")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_layer_norm_parameters(gpu, dtype):
+    """No weight, no bias, parameters of each type, strided and unaligned rows."""
+    x = randn(23, 50, 333, dtype=dtype, std=3.0)
+    for pd in DTYPES:
+        w, b = randn(24, 333, dtype=pd), randn(25, 333, dtype=pd)
+        for weight, bias in ((w, b), (w, None), (None, b), (None, None)):
+            ry, _, _, n = plain_norm(x, weight, bias, 1e-5)
+            y, _, _ = A.layer_norm(strided(x), weight, bias)
+            bound, _ = norm_bounds(ry, n, weight, bias, dtype)
+            within(y, ry, bound, f"{pd} {weight is not None} {bias is not None}")
+            out = strided(torch.zeros_like(x), 3)
+            got = A.layer_norm(unaligned(x), weight, bias, out=out)[0]
+            assert got.data_ptr() == out.data_ptr() and torch.equal(out, y)
+            assert bool(out._base[:, :2].isnan().all()) and bool(out._base[:, -1].isnan().all())
+
+
+def test_layer_norm_hard_rows(gpu):
+    """A large mean, constant rows, huge and tiny values, and rows with
+    infinities and NaN, which stay in their rows."""
+    x = randn(26, 12, 1000)
+    x[1] += 1000.0
+    x[2] = 7.0
+    x[3] = 0.0
+    x[4] *= 1e15
+    x[5] *= 1e-18
+    x[6, 3] = float("inf")
+    x[7, 999] = float("nan")
+    x[8] = -x[8].abs() * 1e4
+    x[9, :999] = 0.0
+    x[9, 999] = 1e4
+    y, mean, rstd = A.layer_norm(x, eps=1e-30)
+    good = [i for i in range(12) if i not in (2, 3, 6, 7)]
+    ry, rm, rr, n = plain_norm(x, None, None, 1e-30)
+    # the mean's own error, 38 E of the values' mean magnitude, meets the
+    # deviations' first rounding again where the mean is large: second order
+    bound, _ = norm_bounds(ry, n, None, None, F32)
+    within(y[good], ry[good], bound[good], "y")
+    within(mean[good], rm[good], (E * rm.abs() + N_ERR / rr)[good], "mean")
+    within(rstd[good], rr[good], (N_ERR * rr)[good], "rstd")
+    assert bool((y[2:4] == 0).all()) and float(mean[2]) == 7.0 and float(mean[3]) == 0.0
+    assert bool(y[6:8].isnan().all())
+
+
+def plain_norm_grad(dy, n, rstd, weight):
+    dy, n, r = dy.double(), n.double(), rstd.double()[..., None]
+    g = dy if weight is None else dy * weight.double()
+    dx = r * (g - g.mean(-1, keepdim=True) - n * (g * n).mean(-1, keepdim=True))
+    flat = lambda t: t.reshape(-1, t.size(-1))  # noqa: E731
+    # n is off by two roundings, g by one; the row sums as above
+    mag_x = r * E * (5 * g.abs() + 44 * g.abs().mean(-1, keepdim=True) +
+                     n.abs() * 50 * (g * n).abs().mean(-1, keepdim=True))
+    # chains of dweight and dbias: the rows of a wave, then three waves, then fp64
+    return dx, flat(dy * n).sum(0), flat(dy).sum(0), mag_x, flat(dy * n).abs().sum(0), flat(dy).abs().sum(0)
+
+
+def chain(rows, hidden):
+    """Rows that one wave or workgroup of the backward pass adds up."""
+    groups = 1024 * 4 if hidden <= 1024 else 1024 if hidden <= 4096 else 256
+    return -(-rows // groups) + 3
+
+
+@pytest.mark.parametrize("kept", [False, True], ids=["x", "kept"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("hidden", WIDTHS)
+def test_layer_norm_grad(gpu, hidden, dtype, kept):
+    for rows in (1, 6, 301):
+        x = randn(30, rows, hidden, dtype=dtype, mean=0.3)
+        dy = randn(31, rows, hidden, dtype=dtype)
+        w = randn(32, hidden, mean=1.0, std=0.3)
+        flush_print(f"layer_norm_grad rows={rows} hidden={hidden} {dtype} kept={kept}")
+        if kept:
+            _, rstd, codes, scales = A.layer_norm_keep(x, w)
+            n = A.checkpoint_unpack(codes, scales, F32)
+            dx, dw, db = A.layer_norm_keep_grad(dy, codes, scales, rstd, w)
+        else:
+            _, mean, rstd = A.layer_norm(x, w)
+            n = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+            dx, dw, db = A.layer_norm_grad(dy, x, mean, rstd, w)
+        rx, rw, rb, mx, mw, mb = plain_norm_grad(dy, n, rstd, w)
+        within(dx, rx, mx + (U[dtype] + E) * rx.abs() + TINY[dtype], "dx")
+        c = chain(rows, hidden)
+        within(dw, rw, (c + 4) * E * mw + E * rw.abs(), "dweight")
+        within(db, rb, c * E * mb + E * rb.abs(), "dbias")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_layer_norm_grad_into_segments(gpu, dtype):
+    rows, hidden = 211, 77
+    x, dy = strided(randn(33, rows, hidden, dtype=dtype)), strided(randn(34, rows, hidden, dtype=dtype), 9)
+    w = randn(35, hidden, dtype=dtype)
+    _, mean, rstd = A.layer_norm(x, w)
+    flat = torch.full((2 * hidden + 9,), 1.5, dtype=dtype, device="cuda")
+    dw, db = flat[3:3 + hidden], flat[3 + hidden:3 + 2 * hidden]
+    dxo = strided(torch.zeros(rows, hidden, dtype=dtype, device="cuda"))
+    n = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    rx, rw, rb, mx, mw, mb = plain_norm_grad(dy, n, rstd, w)
+    dx, _, _ = A.layer_norm_grad(dy, x, mean, rstd, w, dx=dxo, dweight=dw, dbias=db)
+    within(dx, rx, mx + (U[dtype] + E) * rx.abs() + TINY[dtype], "dx")
+    within(dw, rw, 10 * E * mw + (U[dtype] + E) * rw.abs() + TINY[dtype], "dweight")
+    old_w, old_b = dw.clone().double(), db.clone().double()
+    A.layer_norm_grad(dy, x, mean, rstd, w, dx=dxo, dweight=dw, dbias=db, accumulate=True)
+    within(dw, old_w + rw, 10 * E * mw + (U[dtype] + E) * (old_w + rw).abs() + TINY[dtype], "dweight added")
+    within(db, old_b + rb, 10 * E * mb + (U[dtype] + E) * (old_b + rb).abs() + TINY[dtype], "dbias added")
+    assert bool((flat[:3] == 1.5).all()) and bool((flat[3 + 2 * hidden:] == 1.5).all())
+    assert bool(dxo._base[:, :2].isnan().all()) and bool(dxo._base[:, -3:].isnan().all())
+    # without weight: dx alone, no workspace
+    dx0, none_w, none_b = A.layer_norm_grad(dy, x, mean, rstd)
+    r0 = plain_norm_grad(dy, n, rstd, None)
+    within(dx0, r0[0], r0[3] + (U[dtype] + E) * r0[0].abs() + TINY[dtype], "dx without weight")
+    assert none_w is None and none_b is None
+
+
+def test_layer_norm_grad_against_differences(gpu):
+    """The gradient of sum(c * y) along random directions, against central
+    differences of the formula in 64 bits."""
+    rows, hidden, h = 40, 129, 1e-5
+    x, w, b, c = randn(36, rows, hidden), randn(37, hidden), randn(38, hidden), randn(39, rows, hidden)
+    _, mean, rstd = A.layer_norm(x, w, b, eps=1e-5)
+    dx, dw, db = A.layer_norm_grad(c, x, mean, rstd, w)
+
+    def loss(x_, w_, b_):
+        m = x_.mean(1, keepdim=True)
+        v = (x_ - m).square().mean(1, keepdim=True)
+        return float((c.double() * ((x_ - m) / torch.sqrt(v + 1e-5) * w_ + b_)).sum())
+
+    xd, wd, bd = x.double(), w.double(), b.double()
+    for seed in range(4):
+        px, pw, pb = (randn(40 + 3 * seed + i, *t.shape).double() for i, t in enumerate((x, w, b)))
+        num = (loss(xd + h * px, wd + h * pw, bd + h * pb) - loss(xd - h * px, wd - h * pw, bd - h * pb)) / (2 * h)
+        parts = [(dx.double() * px), (dw.double() * pw), (db.double() * pb)]
+        ana = sum(float(p.sum()) for p in parts)
+        # the kernel's roundings, 100 E of the terms' magnitude; the
+        # differences', about 1e-16 / h of the loss's, and h^2 of curvature
+        mag = sum(float(p.abs().sum()) for p in parts)
+        assert abs(num - ana) <= (100 * E + 1e-10 + 1e-15 / h) * mag + 1e-15 / h * float(c.abs().sum()), (num, ana)
+
+
+# ---------------------------------------------------------------- 8 bits
+
+
+def plain_pack(x, top):
+    """Codes and scales by the definition, in exact arithmetic (fp64 powers of two)."""
+    x = x.double().cpu().numpy()
+    rows, width = x.shape
+    nb = -(-width // 32)
+    codes, scales = np.zeros((rows, width), np.int64), np.zeros((rows, nb), np.int64)
+    for r in range(rows):
+        for k in range(nb):
+            v = x[r, 32 * k:32 * k + 32]
+            if not np.isfinite(v).all():
+                scales[r, k] = 255
+                continue
+            e = -127
+            while e < top and np.abs(v).max() > 127 * 2.0 ** e:
+                e += 1
+            scales[r, k] = e + 127
+            codes[r, 32 * k:32 * k + 32] = np.clip(np.rint(v / 2.0 ** e), -127, 127)
+    return codes, scales
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("rows,width", [(1, 1), (1, 31), (3, 32), (2, 33), (7, 64), (5, 100), (17, 257), (2, 4100)])
+def test_checkpoint_pack(gpu, rows, width, dtype):
+    flush_print(f"checkpoint rows={rows} width={width} {dtype}")
+    top = 9 if dtype == F16 else 121
+    x = randn(50, rows, width, dtype=dtype)
+    spread = (torch.rand(rows, width, generator=gen(51), dtype=torch.float64) * 20 - 10).exp2().cuda()
+    for values in (x, (x.double() * spread).to(dtype), torch.zeros_like(x),
+                   (torch.randint(-127, 128, (rows, width), generator=gen(52)).cuda() * 0.25).to(dtype),
+                   # halves of a step: ties go to the even code
+                   (torch.randint(-253, 254, (rows, width), generator=gen(53)).cuda() * 0.5).to(dtype)):
+        want_c, want_s = plain_pack(values, top)
+        for v in (values, strided(values), unaligned(values, 3)):
+            codes, scales = A.checkpoint_pack(v)
+            assert np.array_equal(codes.cpu().numpy(), want_c)
+            assert np.array_equal(scales.cpu().numpy(), want_s)
+        exact = want_c * 2.0 ** (np.repeat(want_s, 32, 1)[:, :width] - 127.0)
+        for out in DTYPES:
+            got = A.checkpoint_unpack(codes, scales, out)
+            want = torch.from_numpy(exact).to(out)  # exact, but for fp16 out of fp16's range
+            assert torch.equal(got.cpu(), want), out
+        o = strided(torch.zeros(rows, width, dtype=dtype, device="cuda"))
+        assert torch.equal(A.checkpoint_unpack(codes, scales, dtype, out=o), A.checkpoint_unpack(codes, scales, dtype))
+        assert bool(o._base[:, :2].isnan().all()) and bool(o._base[:, -3:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_checkpoint_edges_of_the_format(gpu, dtype):
+    """The largest and smallest values, magnitudes at the border between two
+    steps, infinities and NaN; nothing finite reads back as an infinity."""
+    fi = torch.finfo(dtype)
+    sub = fi.smallest_normal * fi.eps
+    rows = [[fi.max, -fi.max, fi.max / 3], [fi.smallest_normal, -fi.smallest_normal / 2, 0.0], [sub, -sub, 0.0],
+            [127.0, 1.0, -0.5], [float(np.nextafter(np.float32(127), np.float32(200))), 1.0, 0.5], [127.5, 1.5, -2.5],
+            [128.0, 3.0, -5.0], [63.5, 0.25, 0.75], [float("inf"), 1.0, 2.0], [1.0, float("nan"), 2.0],
+            [float("-inf"), float("nan"), 0.0], [-0.0, 0.0, 0.0]]
+    x = torch.zeros(len(rows), 70, dtype=torch.float64)
+    for i, r in enumerate(rows):
+        x[i, 30:33] = torch.tensor(r, dtype=torch.float64)  # across two blocks
+        x[i, 66:69] = torch.tensor(r, dtype=torch.float64)
+    x = x.to(dtype).cuda()
+    codes, scales = A.checkpoint_pack(x)
+    want_c, want_s = plain_pack(x, 9 if dtype == F16 else 121)
+    assert np.array_equal(codes.cpu().numpy(), want_c) and np.array_equal(scales.cpu().numpy(), want_s)
+    back = A.checkpoint_unpack(codes, scales, dtype)
+    block = torch.zeros(len(rows), 96, dtype=torch.float64)
+    block[:, :70] = x.double().cpu()
+    amax = block.view(-1, 3, 32).abs().amax(2).repeat_interleave(32, 1)[:, :70]
+    fine = torch.isfinite(amax)
+    assert torch.equal(back.cpu().isnan(), ~fine)
+    assert bool(torch.isfinite(back.cpu()[fine]).all())
+    # half a step, at most 1/127 of the block's largest; 2^-127 is the least step
+    err = (back.double().cpu() - x.double().cpu()).abs()
+    assert bool((err[fine] <= amax[fine] / 127 + 2.0 ** -128).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("hidden", WIDTHS)
+def test_layer_norm_keep(gpu, hidden, dtype):
+    """y and rstd are layer_norm's bits; the kept rows are the normalised ones
+    within half a step, their step the least that reaches the block's largest."""
+    rows = 19
+    x = randn(60, rows, hidden, dtype=dtype, mean=-0.4)
+    w, b = randn(61, hidden), randn(62, hidden)
+    y, rstd, codes, scales = A.layer_norm_keep(x, w, b)
+    y0, _, rstd0 = A.layer_norm(x, w, b)
+    assert torch.equal(y, y0) and torch.equal(rstd, rstd0)
+    n = plain_norm(x, None, None, 1e-5)[3].cpu()
+    dn = N_ERR * (n.abs() + 1)
+    nb = -(-hidden // 32)
+    wide = torch.zeros(rows, nb * 32, dtype=torch.float64)
+    wide[:, :hidden] = n
+    amax = wide.view(rows, nb, 32).abs().amax(2)
+    step = torch.exp2(scales.cpu().double() - 127)
+    slack = N_ERR * (amax + 1)
+    assert bool((127 * step >= amax - slack).all())
+    assert bool(((127 * step / 2 <= amax + slack) | (scales.cpu() == 0)).all())
+    got = A.checkpoint_unpack(codes, scales).cpu().double()
+    assert bool(((got - n).abs() <= step.repeat_interleave(32, 1)[:, :hidden] / 2 + dn).all())
+
+
+# ---------------------------------------------------------------- linear gradient
+
+
+def linear_case(seed, rows, out, width, dtype):
+    dy = randn(seed, rows, out, dtype=dtype)
+    codes, scales = A.checkpoint_pack(randn(seed + 1, rows, width, dtype=dtype))
+    return dy, codes, scales, A.checkpoint_unpack(codes, scales, F32).double()
+
+
+def linear_bound(dy, x, rows, dtype):
+    """Every matrix instruction adds 32 exact products to an fp32 sum: two
+    roundings, each at most 2^-23 of the magnitudes so far (a cut-off instead
+    of a rounding is allowed for); fp32 dy takes three.  dbias: a thread adds
+    all its rows, the threads' sums follow."""
+    parts = 3 if dtype == F32 else 1
+    steps = -(-rows // 32) * parts + 2
+    d = dy.double()
+    return (d.t().abs() @ x.abs()) * (2 * steps * 2.0 ** -23), d.abs().sum(0) * (rows / 4 + 12) * E
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("rows,out,width", [(1, 1, 1), (1, 130, 70), (2, 5, 33), (31, 128, 128), (33, 129, 127),
+                                            (64, 64, 256), (65, 3, 1001), (500, 200, 300), (1025, 131, 37),
+                                            (4096, 256, 128), (9999, 17, 65)])
+def test_linear_grad(gpu, rows, out, width, dtype):
+    flush_print(f"linear_grad rows={rows} out={out} in={width} {dtype}")
+    dy, codes, scales, x = linear_case(70, rows, out, width, dtype)
+    rw, rb = dy.double().t() @ x, dy.double().sum(0)
+    bw, bb = linear_bound(dy, x, rows, dtype)
+    for grad in {F32, dtype}:
+        dw, db = A.linear_grad(dy, codes, scales, dtype=grad)
+        within(dw, rw, bw + (U[grad] + E) * rw.abs() + TINY[grad], f"dweight {grad}")
+        within(db, rb, bb + (U[grad] + E) * rb.abs() + TINY[grad], f"dbias {grad}")
+        again = A.linear_grad(strided(dy), codes, scales, dtype=grad, bias=False)
+        assert torch.equal(again[0], dw) and again[1] is None
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("rows", [100, 3000])
+def test_linear_grad_into_segments(gpu, rows, dtype):
+    out, width = 61, 93
+    dy, codes, scales, x = linear_case(72, rows, out, width, dtype)
+    rw, rb = dy.double().t() @ x, dy.double().sum(0)
+    bw, bb = linear_bound(dy, x, rows, dtype)
+    flat = torch.full((out * width + out + 9,), -0.5, dtype=dtype, device="cuda")
+    dw, db = flat[5:5 + out * width], flat[5 + out * width:5 + out * width + out]
+    A.linear_grad(dy, codes, scales, dweight=dw, dbias=db)
+    within(dw.view(out, width), rw, bw + (U[dtype] + E) * rw.abs() + TINY[dtype], "dweight")
+    old_w, old_b = dw.clone().double().view(out, width), db.clone().double()
+    A.linear_grad(unaligned(dy), unaligned(codes, 3), unaligned(scales, 1), dweight=dw, dbias=db, accumulate=True)
+    within(dw.view(out, width), old_w + rw, bw + (U[dtype] + E) * (old_w + rw).abs() + TINY[dtype], "dweight added")
+    within(db, old_b + rb, bb + (U[dtype] + E) * (old_b + rb).abs() + TINY[dtype], "dbias added")
+    assert bool((flat[:5] == -0.5).all()) and bool((flat[-4:] == -0.5).all())
+
+
+def test_linear_grad_exact_cases(gpu):
+    """Whole numbers whose sums fp32 holds come out exactly: operand layouts,
+    the three parts of fp32 values, split rows."""
+    rows, out, width = 2500, 70, 140
+    g = gen(74)
+    xi = torch.randint(-3, 4, (rows, width), generator=g).double()
+    for dtype, top in ((F32, 60000), (F16, 200), (BF16, 100)):
+        # fp32: 16-bit whole numbers, which a single bf16 cannot hold; sums < 2^24 for the narrow rows
+        di = torch.randint(-top, top + 1, (rows, out), generator=g).double()
+        if dtype == F32:
+            di[torch.rand(rows, out, generator=g) < 0.97] = 0
+        codes, scales = A.checkpoint_pack(xi.to(dtype).cuda())
+        dw, db = A.linear_grad(di.to(dtype).cuda(), codes, scales, dtype=F32)
+        want = di.t() @ xi
+        mag = di.abs().t() @ xi.abs()
+        assert float(mag.max()) < 2 ** 24
+        assert torch.equal(dw.double().cpu(), want) and torch.equal(db.double().cpu(), di.sum(0))
+
+
+def test_linear_grad_infinities_and_nan(gpu):
+    """An infinity or NaN of dy stays in its output row, a block without finite
+    values in its columns."""
+    rows, out, width = 200, 40, 96
+    for dtype in DTYPES:
+        x = randn(76, rows, width, dtype=dtype).abs() + 1
+        x[150, 40] = float("inf")
+        codes, scales = A.checkpoint_pack(x)
+        dy = randn(77, rows, out, dtype=dtype)
+        ref = A.linear_grad(dy, codes, scales, dtype=F32)
+        cols = torch.zeros(width, dtype=torch.bool, device="cuda")
+        cols[32:64] = True
+        assert bool(ref[0][:, cols].isnan().all()) and bool(torch.isfinite(ref[0][:, ~cols]).all())
+        dy2 = dy.clone()
+        dy2[11, 5], dy2[60, 6] = float("inf"), float("nan")
+        dw, db = A.linear_grad(dy2, codes, scales, dtype=F32)
+        assert bool((dw[5, ~cols].abs() == float("inf")).all()) and bool(dw[6].isnan().all())
+        others = [o for o in range(out) if o not in (5, 6)]
+        assert torch.equal(dw[others][:, ~cols], ref[0][others][:, ~cols])
+        assert float(db[5]) == float("inf") and bool(db[6].isnan())
+        assert torch.equal(db[others], ref[1][others])
+
+
+def test_linear_and_embedding_gradients_against_differences(gpu):
+    """Both are linear in the parameter, so a difference of the loss over any
+    step is exact up to rounding."""
+    rows, out, width, vocab = 300, 20, 48, 30
+    dy, codes, scales, x = linear_case(78, rows, out, width, F32)
+    dw, db = A.linear_grad(dy, codes, scales)
+    pw, pb = randn(79, out, width).double(), randn(80, out).double()
+    loss = lambda w, b: float((dy.double() * (x @ w.t() + b)).sum())  # noqa: E731
+    num = (loss(pw, pb) - loss(-pw, -pb)) / 2
+    mag = float((dy.double().abs() * (x.abs() @ pw.abs().t() + pb.abs())).sum())
+    assert abs(num - float((dw.double() * pw).sum() + (db.double() * pb).sum())) <= 100 * E * mag
+    t = tokens_of(81, rows, vocab, "outside")
+    g = A.embedding_grad(dy, t, vocab, scale=3.0)
+    pt = randn(82, vocab, out).double()
+    loss = lambda tab: float((dy.double() * plain_embedding(tab, t, 3.0)).sum())  # noqa: E731
+    num = (loss(pt) - loss(-pt)) / 2
+    mag = float((dy.double().abs() * plain_embedding(pt.abs(), t, 3.0)).sum())
+    assert abs(num - float((g.double() * pt).sum())) <= 100 * E * mag
+
+
+# ---------------------------------------------------------------- as a user runs them
+
+
+def all_calls(seed, dtype=F32):
+    """One call of each operator; returns a function that runs them all and
+    gives their outputs."""
+    n, vocab, hidden, out = 700, 90, 136, 72
+    table = randn(seed, vocab, hidden, dtype=dtype)
+    tok = tokens_of(seed + 1, n, vocab, "frequent")
+    w, b = randn(seed + 2, hidden, mean=1.0), randn(seed + 3, hidden)
+    dz = randn(seed + 4, n, out, dtype=dtype)
+
+    def run(**kw):
+        x = A.embedding(table, tok, scale=2.0, **kw)
+        y, mean, rstd = A.layer_norm(x, w, b, **kw)
+        y2, rstd2, kc, ks = A.layer_norm_keep(x, w, b, **kw)
+        c, s = A.checkpoint_pack(y, **kw)
+        back = A.checkpoint_unpack(c, s, dtype, **kw)
+        dw, db = A.linear_grad(dz, c, s, **kw)
+        d1 = A.layer_norm_grad(back, x, mean, rstd, w, **kw)
+        d2 = A.layer_norm_keep_grad(back, kc, ks, rstd2, w, **kw)
+        g = A.embedding_grad(d1[0], tok, vocab, scale=2.0, **kw)
+        return [x, y, mean, rstd, y2, kc, ks, c, s, back, dw, db, *d1, *d2, g]
+    run.inputs = (table, tok, w, b, dz)
+    return run
+
+
+def same(a, b):
+    return all(torch.equal(p.view(torch.uint8) if p.is_floating_point() else p,
+                           q.view(torch.uint8) if q.is_floating_point() else q) for p, q in zip(a, b, strict=True))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_repeatable_and_on_other_streams(gpu, dtype):
+    run = all_calls(90, dtype)
+    first = run()
+    torch.cuda.synchronize()
+    assert same(first, run())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+        got.append(run(stream=st))
+        # the caller's stream goes on allocating meanwhile
+        junk = [torch.full((1 << 18,), float("nan"), device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del junk
+    assert same(first, got[0]) and same(first, got[1])
+    with torch.cuda.stream(streams[0]):
+        assert same(first, run())
+
+
+def test_captured_and_replayed(gpu):
+    """Two graphs of all operators, captured on the first call, replayed in
+    turn with new inputs and eager work between."""
+    runs = [all_calls(100, BF16), all_calls(110, F32)]
+    graphs, outs = [], []
+    for run in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run())
+        graphs.append(g)
+    for turn in range(4):
+        for i, run in enumerate(runs):
+            table, tok, w, b, dz = run.inputs
+            table.mul_(1.25)
+            tok.copy_(tok.roll(turn + 1))
+            dz.add_(0.125)
+            eager = run()
+            torch.cuda.synchronize()
+            graphs[i].replay()
+            graphs[1 - i].replay()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert same(eager, outs[i]), (turn, i)
+
+
+def test_two_threads(gpu):
+    import threading
+    runs = [all_calls(120, BF16), all_calls(130, F16)]
+    want = [r() for r in runs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        for _ in range(5):
+            got = runs[i](stream=st)
+            st.synchronize()
+            if not same(want[i], got):
+                bad.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_workspace_of_the_caller(gpu):
+    lib = _native.lib()
+    n, vocab, hidden = 900, 20, 65
+    tok, dy = tokens_of(140, n, vocab, "frequent"), randn(141, n, hidden)
+    need = lib.adasum_embedding_grad_workspace_bytes(n, hidden, 0)
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    got = A.embedding_grad(dy, tok, vocab, workspace=ws[:need])
+    assert torch.equal(got, A.embedding_grad(dy, tok, vocab))
+    assert bool((ws[need:] == 255).all())
+    with pytest.raises(A.AdasumError, match="workspace too small"):
+        A.embedding_grad(dy, tok, vocab, workspace=ws[:need - 256])
+    x, w = randn(142, n, hidden), randn(143, hidden)
+    _, mean, rstd = A.layer_norm(x, w)
+    need = lib.adasum_layer_norm_grad_workspace_bytes(n, hidden, 0)
+    ws.fill_(255) if ws.numel() >= need + 64 else None
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    assert same(A.layer_norm_grad(dy, x, mean, rstd, w, workspace=ws[:need]), A.layer_norm_grad(dy, x, mean, rstd, w))
+    assert bool((ws[need:] == 255).all())
+    codes, scales = A.checkpoint_pack(x)
+    need = lib.adasum_linear_grad_workspace_bytes(n, hidden, hidden, 0)
+    assert need > 0
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    assert same(A.linear_grad(dy, codes, scales, workspace=ws[:need]), A.linear_grad(dy, codes, scales))
+    assert bool((ws[need:] == 255).all())
+
+
+def test_python_refusals(gpu):
+    x = randn(150, 6, 40)
+    w = randn(151, 40)
+    t = torch.zeros(6, dtype=torch.int64, device="cuda")
+    y, mean, rstd = A.layer_norm(x, w)
+    c, s = A.checkpoint_pack(x)
+    bad = [
+        lambda: A.embedding(x, t.float()),
+        lambda: A.embedding(x, t.cpu()),
+        lambda: A.embedding(x[0], t),
+        lambda: A.embedding(x.t(), t),
+        lambda: A.embedding(x.double(), t),
+        lambda: A.embedding(x, torch.zeros(12, dtype=torch.int64, device="cuda")[::2]),
+        lambda: A.embedding(x, t, out=torch.empty(6, 41, device="cuda")),
+        lambda: A.embedding_grad(x, t[:5], 9),
+        lambda: A.embedding_grad(x, t, 9, accumulate=True),
+        lambda: A.embedding_grad(x, t, 9, out=torch.empty(9, 39, device="cuda")),
+        lambda: A.embedding_grad(x[:1].expand(6, 40), t, 9),
+        lambda: A.layer_norm(x, w[:39]),
+        lambda: A.layer_norm(x, w, w.half()),
+        lambda: A.layer_norm(torch.empty(3, 0, device="cuda")),
+        lambda: A.layer_norm(x.t()),
+        lambda: A.layer_norm_grad(x, x.half(), mean, rstd, w),
+        lambda: A.layer_norm_grad(x, x, mean[:5], rstd, w),
+        lambda: A.layer_norm_grad(x, x, mean.double(), rstd, w),
+        lambda: A.layer_norm_grad(x, None, None, rstd, w),
+        lambda: A.layer_norm_grad(x, x, mean, rstd, w, accumulate=True),
+        lambda: A.layer_norm_grad(x, x, mean, rstd, None, dweight=w),
+        lambda: A.layer_norm_grad(x, x, mean, rstd, w, dweight=w.clone(), dbias=w.half()),
+        lambda: A.layer_norm_keep_grad(x, c[:, :39].contiguous(), s, rstd, w),
+        lambda: A.layer_norm_keep_grad(x, c, s[:, :1].contiguous(), rstd, w),
+        lambda: A.checkpoint_unpack(c, s.to(torch.int32)),
+        lambda: A.checkpoint_unpack(c, s, torch.float64),
+        lambda: A.linear_grad(x[:5], c, s),
+        lambda: A.linear_grad(x, c, s, accumulate=True),
+        lambda: A.linear_grad(x, c, s, dweight=torch.empty(40, 39, device="cuda")),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            flush_print("not refused:", i)
+    flat = torch.zeros(2000, device="cuda")
+    overlapping = [
+        lambda: A.layer_norm(flat[:240].view(6, 40), out=flat[100:340].view(6, 40)),
+        lambda: A.layer_norm_grad(x, x, mean, rstd, w, dx=x),
+        lambda: A.embedding(flat[:400].view(10, 40), t, out=flat[200:440].view(6, 40)),
+        lambda: A.checkpoint_unpack(c, s, out=c.view(-1)[:240].view(torch.float32).new_empty(0).view(0, 40)),
+        lambda: A.linear_grad(x, c, s, dweight=flat[:1600].view(40, 40), dbias=flat[1599:1639]),
+    ]
+    for i, f in enumerate(overlapping):
+        with pytest.raises((A.AdasumError, ValueError)):
+            f()
+            flush_print("not refused:", i)
+
+
+def test_offsets_past_32_bits(gpu):
+    """Rows so far apart that element offsets pass 2^32."""
+    rows, width, stride = 1100, 50, 1 << 22
+    assert (rows - 1) * stride > 2 ** 32
+    big = torch.empty((rows - 1) * stride + width, dtype=BF16, device="cuda")
+    x = big.as_strided((rows, width), (stride, 1))
+    x.copy_(randn(160, rows, width, dtype=BF16))
+    near = x.contiguous()
+    tok = tokens_of(161, rows, 30, "uniform")
+    w = randn(162, width)
+    assert torch.equal(A.embedding_grad(x, tok, 30, dtype=F32), A.embedding_grad(near, tok, 30, dtype=F32))
+    assert torch.equal(A.embedding(x, tok + rows - 30), A.embedding(near, tok + rows - 30))
+    far, close = A.layer_norm(x, w), A.layer_norm(near, w)
+    assert same(far, close)
+    assert same(A.layer_norm_keep(x, w), A.layer_norm_keep(near, w))
+    assert same(A.layer_norm_grad(x, near, *close[1:], w), A.layer_norm_grad(near, x, *close[1:], w))
+    packed = A.checkpoint_pack(x)
+    assert same(packed, A.checkpoint_pack(near))
+    assert same(A.linear_grad(x, *packed, dtype=F32), A.linear_grad(near, *packed, dtype=F32))
+    x.zero_()
+    assert torch.equal(A.checkpoint_unpack(*packed, BF16, out=x), A.checkpoint_unpack(*packed, BF16))
+    x.zero_()
+    A.embedding(near, tok, out=x)
+    assert torch.equal(x, A.embedding(near, tok))
+    x.zero_()
+    A.layer_norm(near, w, out=x)
+    assert torch.equal(x, close[0])
+
+
+def test_workers_gradients_into_the_combine(gpu):
+    """Four workers' microbatches through embedding, norm and a linear layer
+    and back, in two accumulated halves, every gradient written into its
+    segment of the worker's buffer; the combined gradient against the oracle
+    on the same steps in 64 bits."""
+    K, n, vocab, hidden, out = 4, 512, 200, 96, 72
+    lengths = [vocab * hidden, hidden, hidden, out * hidden, out]
+    off = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int64)
+    table = randn(170, vocab, hidden, std=0.05)
+    w, b = randn(171, hidden, mean=1.0, std=0.1), randn(172, hidden, std=0.1)
+    lin = randn(173, out, hidden, std=0.1)
+    scale = math.sqrt(hidden)
+    flats, exact = [], []
+    for k in range(K):
+        tok = tokens_of(180 + k, n, vocab, "outside")
+        dz = randn(190 + k, n, out, std=1e-2)
+        flat = torch.empty(int(off[-1]), device="cuda")
+        segs = [flat[off[i]:off[i + 1]] for i in range(5)]
+        ref = [torch.zeros(l, dtype=torch.float64, device="cuda") for l in lengths]
+        for half in range(2):
+            t, d = tok[half * 256:][:256], dz[half * 256:][:256]
+            acc = half == 1
+            x = A.embedding(table, t, scale=scale)
+            y, rstd, codes, scales = A.layer_norm_keep(x, w, b)
+            yc, ys = A.checkpoint_pack(y)
+            del x
+            A.linear_grad(d, yc, ys, dweight=segs[3], dbias=segs[4], accumulate=acc)
+            dy = d @ lin
+            dx, _, _ = A.layer_norm_keep_grad(dy, codes, scales, rstd, w, dweight=segs[1], dbias=segs[2],
+                                              accumulate=acc)
+            A.embedding_grad(dx, t, vocab, scale=scale, out=segs[0], accumulate=acc)
+            # the same in 64 bits, from the rows as they were kept
+            nk, yk = A.checkpoint_unpack(codes, scales).double(), A.checkpoint_unpack(yc, ys).double()
+            dyd = d.double() @ lin.double()
+            dxd, dwd, dbd, *_ = plain_norm_grad(dyd, nk, rstd, w)
+            ref[0] += plain_embedding_grad(dxd, t, vocab, scale)[0].cuda().view(-1)
+            ref[1] += dwd
+            ref[2] += dbd
+            ref[3] += (d.double().t() @ yk).reshape(-1)
+            ref[4] += d.double().sum(0)
+        flats.append(flat)
+        exact.append(torch.cat(ref).cpu().numpy())
+    got = A.combine(flats, off).double().cpu().numpy()
+    want = oracle.combine(exact, off, out_format="f32")["out"]
+    for i in range(5):
+        a, c = got[off[i]:off[i + 1]], want[off[i]:off[i + 1]]
+        err = float(np.linalg.norm(a - c) / np.linalg.norm(c))
+        flush_print(f"  segment {i}: relative L2 {err:.3g}")
+        assert err <= 1e-5  # the combine's own tolerance; fp32 gradients are off by about 1e-6
