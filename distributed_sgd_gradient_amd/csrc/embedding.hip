@@ -217,7 +217,9 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
       for (int j = 0; j < 4; ++j) want[j] = __ballot(t[j] >= 0 && (t[j] & mask) == g);
       // one token of this step after another: its rows' places are by lane,
       // then by place in the lane
-      while (uint64_t left = want[0] | want[1] | want[2] | want[3]) {
+      for (int turn = 0; turn < 256; ++turn) {  // at most 256 tokens
+        const uint64_t left = want[0] | want[1] | want[2] | want[3];
+        if (left == 0) break;
         const int src = __builtin_ctzll(left);
         int pick = t[3];
 #pragma unroll
@@ -238,8 +240,10 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if ((eq[j] >> lane) & 1u) {
-            a.rows[pos] = (int32_t)(at + j);
-            a.grouped[pos] = token;
+            if (pos >= 0 && pos < a.n) {
+              a.rows[pos] = (int32_t)(at + j);
+              a.grouped[pos] = token;
+            }
             ++pos;
           }
         // the wave's own counter: every lane has read it before lane 0 moves
@@ -259,7 +263,7 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
 
 struct RunArgs {
   const void* dy;
-  int64_t dy_stride;
+  int64_t n, dy_stride, vocab;
   int hidden, span, lanes_shift;
   const int32_t* rows;
   const int32_t* grouped;
@@ -272,22 +276,54 @@ struct RunArgs {
   int64_t pitch;
 };
 
+// The grouped list as the summing kernels read it: whatever it holds, they
+// stay inside dy and grad.  It is right as long as the tokens do not change
+// between the grouping kernel's two scans; a caller that breaks this gets
+// wrong sums, not accesses out of bounds.
+__device__ __forceinline__ int64_t listed_rows(const RunArgs& a) {
+  const int64_t m = *a.count;
+  return m < 0 ? 0 : m < a.n ? m : a.n;
+}
+__device__ __forceinline__ int32_t listed_token(const RunArgs& a, int64_t p) {
+  const int32_t t = a.grouped[p];
+  return t >= 0 && t < a.vocab ? t : 0;
+}
+__device__ __forceinline__ int32_t listed_row(const RunArgs& a, int64_t p) {
+  const int32_t r = a.rows[p];
+  return r >= 0 && r < a.n ? r : 0;
+}
+
 constexpr int kSumThreads = 512;
 constexpr int kSumSpots = 2048;  // grouped positions of a workgroup at most
 constexpr int kSumBatch = 8;     // rows a lane has in flight
 
-template <typename O, int N>
-__device__ __forceinline__ void write_gradient(O* p, const float (&s)[N], float scale, int valid, bool accumulate) {
-  float v[N];
+// A lane's N columns of a row.  The last lane of a row whose width is no
+// multiple of N takes the row's last N columns instead, so that every load is
+// a whole vector without a branch; the first `shift` of them belong to the
+// lane before and are not stored.  A width below N is loaded value by value,
+// the last one again in place of those past it.
+template <typename T, int N, bool NARROW>
+__device__ __forceinline__ void load_columns(const T* p, int hidden, float (&v)[N]) {
+  if constexpr (NARROW) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = s[i] * scale;
-  if (accumulate) {
-    float old[N];
-    load_row<O, N>(p, valid, old);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += old[i];
+    for (int i = 0; i < N; ++i) v[i] = (float)p[i < hidden ? i : hidden - 1];
+  } else {
+    load_row<T, N>(p, N, v);
   }
-  store_row<O, N>(p, v, valid);
+}
+template <typename O, int N, bool NARROW>
+__device__ __forceinline__ void store_columns(O* p, const float (&v)[N], int shift, int hidden) {
+  if constexpr (NARROW) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < hidden) p[i] = (O)v[i];
+  } else if (shift == 0) {
+    store_row<O, N>(p, v, N);
+  } else {
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+      if (i >= shift) p[i] = (O)v[i];
+  }
 }
 
 // A workgroup's `units` row groups of 2^lanes_shift lanes each walk `span`
@@ -296,7 +332,7 @@ __device__ __forceinline__ void write_gradient(O* p, const float (&s)[N], float 
 // adds its part of a run begun before it into LDS (`heads`); the run's owner
 // collects these parts in order.  At the workgroup's ends the same is done
 // through memory by the join kernel.
-template <typename T, typename O>
+template <typename T, typename O, bool NARROW, bool ADD>
 __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
   constexpr int VEC = Type<T>::kVec;
   constexpr int N = VEC > Type<O>::kVec ? VEC : Type<O>::kVec;
@@ -308,18 +344,19 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
   const int unit = tid >> a.lanes_shift, lane = tid & (lanes - 1);
   const int spots = units * a.span;
   const int64_t first = (int64_t)blockIdx.x * spots;
-  const int64_t m = *a.count;
+  const int64_t m = listed_rows(a);
   if (first >= m) return;
   const int here = (int)(m - first < spots ? m - first : spots);
   for (int i = tid; i < spots + 2; i += kSumThreads) {
     const int64_t p = first + i - 1;
-    tok[i] = p >= 0 && p < m ? a.grouped[p] : -1;
+    tok[i] = p >= 0 && p < m ? listed_token(a, p) : -1;
   }
-  for (int i = tid; i < here; i += kSumThreads) row[i] = a.rows[first + i];
+  for (int i = tid; i < here; i += kSumThreads) row[i] = listed_row(a, first + i);
   __syncthreads();
 
-  const int col = (int)(blockIdx.y * lanes + lane) * N;
-  const int valid = a.hidden - col;
+  const int want = (int)(blockIdx.y * lanes + lane) * N;
+  const bool any = want < a.hidden;  // the other lanes repeat the last columns and store nothing
+  const int col = NARROW ? 0 : min(want, a.hidden - N), shift = want - col;
   const T* dy = static_cast<const T*>(a.dy) + col;
   O* grad = static_cast<O*>(a.grad) + col;
   const int p0 = unit * a.span;
@@ -328,17 +365,30 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
   float acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  auto write = [&](int t) {
+    if (!any) return;
+    O* p = grad + (int64_t)t * a.hidden;
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = acc[i] * a.scale;
+    if constexpr (ADD) {
+      float old[N];
+      load_columns<O, N, NARROW>(p, a.hidden, old);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += old[i];
+    }
+    store_columns<O, N, NARROW>(p, v, shift, a.hidden);
+  };
   int token = num > 0 ? tok[1 + p0] : -1;
   bool ours = num > 0 && tok[p0] != token;  // this run begins in this row group
   bool head = false;                        // heads[tid] holds the end of a run begun before
   for (int i0 = 0; i0 < num; i0 += kSumBatch) {
     float v[kSumBatch][N];
-    // no branch around the loads: positions past the last read row 0 of the
-    // batch again and are dropped
+    // positions past the last read the batch's first row again and are dropped
 #pragma unroll
     for (int u = 0; u < kSumBatch; ++u) {
       const int i = i0 + u < num ? i0 + u : i0;
-      load_row<T, N>(dy + (int64_t)row[p0 + i] * a.dy_stride, valid, v[u]);
+      load_columns<T, N, NARROW>(dy + (int64_t)row[p0 + i] * a.dy_stride, a.hidden, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kSumBatch; ++u) {
@@ -346,7 +396,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
       const int t = tok[1 + p0 + i0 + u];
       if (t != token) {
         if (ours) {
-          write_gradient<O, N>(grad + (int64_t)token * a.hidden, acc, a.scale, valid, a.accumulate);
+          write(token);
         } else {
           head = true;
 #pragma unroll
@@ -373,32 +423,29 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
   // in row group 0 also of a run begun before the workgroup
   const int64_t spot = (int64_t)blockIdx.x * a.pitch + col;
   auto collect = [&](float (&sum)[N], int t) {
-    int u = unit + 1;
-    for (; u < units && tok[1 + u * a.span] == t && u * a.span < here; ++u) {
+    for (int u = unit + 1; u < units; ++u) {
+      if (u * a.span >= here || tok[1 + u * a.span] != t) break;
 #pragma unroll
       for (int i = 0; i < N; ++i) sum[i] += heads[u * lanes + lane][i];
       // the run ends inside row group u unless its last position has the token
-      const int last = min((u + 1) * a.span, here);
-      if (tok[last] != t) return false;
+      if (tok[min((u + 1) * a.span, here)] != t) return false;
     }
     return true;  // not seen to end inside the workgroup's positions
   };
   if (unit == 0 && head) {
     const int t = tok[1];
-    const int last = min(a.span, here);
     float sum[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) sum[i] = heads[tid][i];
-    if (tok[last] == t) (void)collect(sum, t);
-    if (valid > 0) store_row<float, N>(a.head + spot, sum, N);
+    if (tok[min(a.span, here)] == t) (void)collect(sum, t);
+    if (any) store_columns<float, N, NARROW>(a.head + spot, sum, shift, a.hidden);
   }
   if (ours) {
     const bool on = collect(acc, token) && tok[here + 1] == token;
-    if (on) {
-      if (valid > 0) store_row<float, N>(a.tail + spot, acc, N);
-    } else {
-      write_gradient<O, N>(grad + (int64_t)token * a.hidden, acc, a.scale, valid, a.accumulate);
-    }
+    if (!on)
+      write(token);
+    else if (any)
+      store_columns<float, N, NARROW>(a.tail + spot, acc, shift, a.hidden);
   }
 }
 
@@ -408,32 +455,29 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
 // tail and the heads of the workgroups it reaches, in order, one column a
 // thread.
 __global__ __launch_bounds__(256) void join_runs_kernel(RunArgs a, int spots, int grad_dtype) {
-  const int64_t m = *a.count;
+  const int64_t m = listed_rows(a);
   const int64_t first = (int64_t)blockIdx.x * spots, next = first + spots;
   if (next >= m) return;
-  const int32_t t = a.grouped[next - 1];
-  if (a.grouped[next] != t) return;
+  const int32_t t = listed_token(a, next - 1);
+  if (listed_token(a, next) != t) return;
   // the run's owner is this workgroup unless all its positions belong to a
   // run begun before it
-  if (first > 0 && a.grouped[first] == t && a.grouped[first - 1] == t) return;
+  if (first > 0 && listed_token(a, first) == t && listed_token(a, first - 1) == t) return;
   // workgroups whose first position has the token, found 64 at a time
-  int64_t reach = 0;
-  const int64_t blocks = (m + spots - 1) / spots;
-  for (;;) {
-    const int64_t b = blockIdx.x + 1 + reach + (threadIdx.x & 63);
-    const uint64_t off = ~__ballot(b < blocks && a.grouped[b * spots] == t);
-    if (off != 0) {
-      reach += __builtin_ctzll(off);
-      break;
-    }
-    reach += 64;
+  int reach = 0;
+  const int blocks = (int)((m + spots - 1) / spots);
+  for (int b0 = (int)blockIdx.x + 1; b0 < blocks; b0 += 64) {
+    const int b = b0 + (int)(threadIdx.x & 63);
+    const uint64_t off = ~__ballot(b < blocks && listed_token(a, (int64_t)b * spots) == t);
+    reach += off != 0 ? __builtin_ctzll(off) : 64;
+    if (off != 0) break;
   }
   const int64_t col = (int64_t)blockIdx.y * 256 + threadIdx.x;
   if (col >= a.hidden) return;
   double s = (double)a.tail[blockIdx.x * a.pitch + col];
   const float* head = a.head + ((int64_t)blockIdx.x + 1) * a.pitch + col;
 #pragma unroll 16
-  for (int64_t b = 0; b < reach; ++b) s += (double)head[b * a.pitch];
+  for (int b = 0; b < reach; ++b) s += (double)head[b * a.pitch];
   s *= (double)a.scale;
   const int64_t i = (int64_t)t * a.hidden + col;
   store_any(a.grad, grad_dtype, i, a.accumulate ? s + (double)load_any(a.grad, grad_dtype, i) : s);
@@ -525,7 +569,9 @@ hipError_t launch_embedding_grad(int dtype, const EmbeddingGradArgs& a, hipStrea
 
   RunArgs s{};
   s.dy = a.dy;
+  s.n = a.n;
   s.dy_stride = a.dy_stride;
+  s.vocab = a.vocab;
   s.hidden = a.hidden;
   s.span = l.span;
   while ((1 << s.lanes_shift) < l.lanes) ++s.lanes_shift;
@@ -544,7 +590,15 @@ hipError_t launch_embedding_grad(int dtype, const EmbeddingGradArgs& a, hipStrea
       using O = decltype(o);
       constexpr int N = Type<T>::kVec > Type<O>::kVec ? Type<T>::kVec : Type<O>::kVec;
       const unsigned tiles = (unsigned)ceil_div(a.hidden, (int64_t)l.lanes * N);
-      sum_runs_kernel<T, O><<<dim3((unsigned)l.blocks, tiles), kSumThreads, 0, st>>>(s);
+      const dim3 grid((unsigned)l.blocks, tiles);
+      if (a.hidden < N && a.accumulate)
+        sum_runs_kernel<T, O, true, true><<<grid, kSumThreads, 0, st>>>(s);
+      else if (a.hidden < N)
+        sum_runs_kernel<T, O, true, false><<<grid, kSumThreads, 0, st>>>(s);
+      else if (a.accumulate)
+        sum_runs_kernel<T, O, false, true><<<grid, kSumThreads, 0, st>>>(s);
+      else
+        sum_runs_kernel<T, O, false, false><<<grid, kSumThreads, 0, st>>>(s);
       return hipGetLastError();
     });
   });

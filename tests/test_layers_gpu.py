@@ -149,7 +149,7 @@ def plain_embedding_grad(dy, tokens, vocab, scale):
 @pytest.mark.parametrize("kind", ["uniform", "frequent", "one", "none", "outside"])
 @pytest.mark.parametrize("n,vocab,hidden", [(1, 1, 1), (5, 3, 4), (64, 2, 8), (300, 17, 40), (1023, 700, 129),
                                             (5000, 2, 64), (4097, 1, 1001), (2500, 3001, 3), (20000, 40, 24),
-                                            (9000, 140000, 8)])
+                                            (9000, 140000, 8), (30000, 900, 264), (70000, 30, 16), (25000, 5000, 1031)])
 def test_embedding_grad(gpu, n, vocab, hidden, kind):
     flush_print(f"embedding_grad n={n} vocab={vocab} hidden={hidden} {kind}")
     t = tokens_of(7, n, vocab, kind)
@@ -202,6 +202,30 @@ def test_embedding_grad_into_a_segment(gpu, dtype):
     within(seg.view(vocab, hidden), want, want.abs() * (U[dtype] + 2 * E) + mag * 545 * E + TINY[dtype], "added")
     assert torch.equal(seg.view(vocab, hidden)[3], first[3])
     assert bool((flat[:7] == 2.5).all()) and bool((flat[7 + vocab * hidden:] == 2.5).all())
+
+
+def test_embedding_grad_back_to_back(gpu):
+    """Calls that share a workspace in stream order, each with another number
+    of rows that have a token, nothing waiting between them."""
+    n, vocab, hidden = 30000, 4000, 520
+    dy = randn(13, n, hidden, dtype=BF16)
+    toks = [tokens_of(14 + i, n, vocab, kind) for i, kind in enumerate(("uniform", "outside", "none", "frequent"))]
+    toks[3][1000:] = -1
+    ws = torch.empty(_native.lib().adasum_embedding_grad_workspace_bytes(n, hidden, 2), dtype=torch.uint8,
+                     device="cuda")
+    want = []
+    for t in toks:
+        ws.fill_(0x55)
+        want.append(A.embedding_grad(dy, t, vocab, dtype=F32, workspace=ws))
+        torch.cuda.synchronize()
+        ref, mag = plain_embedding_grad(dy, t, vocab, 1.0)
+        within(want[-1], ref, ref.abs() * 3 * E + mag * 544 * E, "alone")
+    ws.fill_(0x55)
+    order = [0, 1, 2, 3, 0, 3, 2, 1, 1, 0, 2, 0, 3, 1]
+    got = [A.embedding_grad(dy, toks[i], vocab, dtype=F32, workspace=ws) for i in order]
+    torch.cuda.synchronize()
+    for i, g in zip(order, got, strict=True):
+        assert torch.equal(g, want[i])
 
 
 def test_no_rows(gpu):
