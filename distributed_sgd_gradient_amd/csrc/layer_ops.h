@@ -132,12 +132,14 @@ hipError_t launch_embedding_grad(int dtype, const EmbeddingGradArgs& a, hipStrea
 // ---------------------------------------------------------------- linear gradient
 
 // How the gradient's matrix is cut: tiles of the output, and the rows split
-// over `splits` workgroups per tile whose partial sums are joined.
+// over `splits` workgroups per tile whose partial sums are joined (those of
+// dbias from every tile: the tiles of a column of dy share its rows).
 struct LinearGradLayout {
   int64_t tiles_out, tiles_in;
   int splits;
   int64_t split_rows;  // rows of a split, a multiple of the kernel's step
   size_t weight, bias, total;  // byte offsets of the partial sums
+  bool direct;                 // one split whose sums are the gradient as they are
 };
 LinearGradLayout linear_grad_layout(int64_t rows, int64_t out, int64_t in, int dtype);
 

@@ -353,12 +353,13 @@ int checkpoint_unpack(const int8_t* codes, const uint8_t* scales, int64_t rows, 
 
 int check_linear(int64_t rows, int64_t out, int64_t in, int64_t stride, int dtype, size_t* dy_bytes) {
   RETURN_IF(check_matrix(rows, out, stride, dtype, "dy", dy_bytes));
-  if (in < 1 || in >= kMaxDim) return fail(ADASUM_EINVAL, "in_features must be in [1, 2^31)");
+  if (in < 1 || in > kMaxVocab || out > kMaxVocab)
+    return fail(ADASUM_EINVAL, "in_features and out_features must be in [1, 2^24]");
   if (in > kMaxElements / out || (rows > 0 && in > kMaxElements / rows))
     return fail(ADASUM_EINVAL, "linear gradient: over 2^40 elements");
   const LinearGradLayout l = linear_grad_layout(rows, out, in, dtype);
-  // workgroups of a launch: 256 lanes each, 2^32 lanes at most
-  if (l.tiles_out * l.tiles_in >= (int64_t(1) << 24))
+  // workgroups of a launch: 512 lanes each, 2^32 lanes at most
+  if (l.tiles_out * l.tiles_in * l.splits >= (int64_t(1) << 23))
     return fail(ADASUM_EINVAL, "linear gradient: dweight is too large for one call");
   return ADASUM_OK;
 }

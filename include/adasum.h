@@ -333,15 +333,15 @@ ADASUM_API int adasum_checkpoint_unpack(const int8_t* codes, const uint8_t* scal
 /*
  * adasum_linear_grad - the gradient of y = x weight^T + bias from activations
  * kept in 8 bits: dweight[o][i] = sum over rows of dy[r][o] * x[r][i],
- * dbias[o] = sum over rows of dy[r][o].  Products are exact.
+ * dbias[o] = sum over rows of dy[r][o].  Products are exact.  in_features and
+ * out_features are at most 2^24.
  *
  *   dy           rows x out_features elements of dtype.
  *   codes, scales rows x in_features activations packed from dtype (fp16:
  *                their values must be fp16 values, as packed ones are).
  *   dweight      dense, out_features x in_features elements of grad_dtype.
  *   dbias        out_features elements of grad_dtype; NULL: not wanted.
- *   workspace    adasum_linear_grad_workspace_bytes(...) bytes (0 for few
- *                rows, then NULL is allowed).
+ *   workspace    adasum_linear_grad_workspace_bytes(...) bytes.
  */
 ADASUM_API int64_t adasum_linear_grad_workspace_bytes(int64_t rows, int64_t out_features, int64_t in_features,
                                                       int dtype);
