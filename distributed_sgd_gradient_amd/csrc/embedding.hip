@@ -20,6 +20,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.h"
 #include "layer_ops.h"
@@ -76,28 +77,39 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbeddingArgs a) {
 
 constexpr int kGroupWaves = 16;
 constexpr int kGroupKeys = 512;  // most tokens a workgroup of the grouping kernel owns (32 KB of counts)
+constexpr int kNotes = 512;      // owned rows that a wave of the grouping kernel notes
 constexpr int kGroupBatch = 4;   // steps of 256 tokens whose loads a wave has in flight
 
-// The tokens of four consecutive places from p on (i places into the list),
-// those past n or outside the vocabulary as -1.
+// Four consecutive places of the list from i on: for each the token's low
+// bits (those in `mask`), or mask + 1 where it is no token or past n; and the
+// token itself.
 template <typename TOK>
-__device__ __forceinline__ void load_tokens(const TOK* tokens, int64_t i, int64_t n, int64_t vocab, int (&t)[4]) {
-  TOK raw[4];
+__device__ __forceinline__ void load_tokens(const TOK* tokens, int64_t i, int64_t n, uint32_t vocab, uint32_t mask,
+                                            uint32_t (&low)[4], uint32_t (&t)[4]) {
+  uint32_t high[4] = {0u, 0u, 0u, 0u};  // of a token of 64 bits
   if (i + 4 <= n) {
     if constexpr (sizeof(TOK) == 4) {
       const v4u r = load_at<v4u, 4>(tokens + i);
-      raw[0] = (TOK)r.x; raw[1] = (TOK)r.y; raw[2] = (TOK)r.z; raw[3] = (TOK)r.w;
+      t[0] = r.x; t[1] = r.y; t[2] = r.z; t[3] = r.w;
     } else {
-      typedef int64_t v2l __attribute__((ext_vector_type(2)));
-      const v2l r = load_at<v2l, 8>(tokens + i), s = load_at<v2l, 8>(tokens + i + 2);
-      raw[0] = r.x; raw[1] = r.y; raw[2] = s.x; raw[3] = s.y;
+      const v4u r = load_at<v4u, 8>(tokens + i), s = load_at<v4u, 8>(tokens + i + 2);
+      t[0] = r.x; t[1] = r.z; t[2] = s.x; t[3] = s.z;
+      high[0] = r.y; high[1] = r.w; high[2] = s.y; high[3] = s.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) raw[j] = i + j < n ? tokens[i + j] : (TOK)-1;
-  }
+    for (int j = 0; j < 4; ++j) t[j] = ~0u;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) t[j] = raw[j] >= 0 && (int64_t)raw[j] < vocab ? (int)raw[j] : -1;
+    for (int j = 0; j < 4; ++j)
+      if (i + j < n) {
+        const int64_t x = (int64_t)tokens[i + j];
+        t[j] = x >= 0 && x < (int64_t)vocab ? (uint32_t)x : ~0u;
+      }
+  }
+  // a negative token has a sign bit in its low or its high word, and vocab is
+  // far below 2^31
+#pragma unroll
+  for (int j = 0; j < 4; ++j) low[j] = t[j] < vocab && high[j] == 0u ? t[j] & mask : mask + 1u;
 }
 
 struct GroupArgs {
@@ -118,47 +130,72 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
 
 // Workgroup g owns the tokens t with t mod G = g (dealing them by their low
 // bits spreads the frequent ones, which many vocabularies put first).  Its 16
-// waves each scan a sixteenth of the list twice.  The first scan counts, per
-// wave, the rows of every owned token, and the rows of the tokens of lower
-// workgroups: their number is where this workgroup's part of the grouped list
-// begins, so the workgroups need nothing from each other.  The second scan
-// writes the owned rows; a wave's position for a token starts where the
-// counts of the waves before it end, so the rows of a token stay in order.
+// waves each scan a sixteenth of the list.  The scan counts, per wave, the
+// rows of every owned token, and the rows of the tokens of lower workgroups:
+// their number is where this workgroup's part of the grouped list begins, so
+// the workgroups need nothing from each other.  It also notes the owned rows
+// it meets, in order, in LDS.  A wave's position for a token starts where the
+// counts of the waves before it end, so the rows of a token stay in order
+// when the notes are written out.  A wave that met more rows than its notes
+// hold (a token of many rows) scans its part again instead.
 template <typename TOK>
 __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
   extern __shared__ int32_t counts[];  // [16][keys]: counts, then positions
   __shared__ int32_t lower[kGroupWaves], scan[kGroupWaves];
   __shared__ int32_t totals[kGroupKeys];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int G = 1 << a.shift, g = blockIdx.x, keys = a.keys;
+  __shared__ uint32_t note_row[kGroupWaves][kNotes];
+  __shared__ uint16_t note_key[kGroupWaves][kNotes];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const uint32_t G = 1u << a.shift, g = blockIdx.x;
+  const int keys = a.keys;
   const TOK* tokens = static_cast<const TOK*>(a.tokens);
   for (int i = tid; i < kGroupWaves * keys; i += 1024) counts[i] = 0;
   __syncthreads();
 
   const int64_t steps = (a.n + 1024 * 4 - 1) / (1024 * 4);  // of 256 tokens, per wave
   const int64_t begin = wave * steps * 256;
-  const int mask = G - 1;
+  const uint32_t mask = G - 1, vocab = (uint32_t)a.vocab;
   int32_t* mine = counts + wave * keys;
-  auto fetch = [&](int64_t s, int (&t)[kGroupBatch][4]) {
+  auto fetch = [&](int64_t s, uint32_t (&low)[kGroupBatch][4], uint32_t (&t)[kGroupBatch][4])
+                   __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < kGroupBatch; ++u)
-      load_tokens(tokens, s + u < steps ? begin + (s + u) * 256 + lane * 4 : a.n, a.n, a.vocab, t[u]);
+      load_tokens(tokens, s + u < steps ? begin + (s + u) * 256 + lane * 4 : a.n, a.n, vocab, mask, low[u], t[u]);
   };
 
-  int less = 0;
+  int less = 0, noted = 0;  // of the wave
   for (int64_t s = 0; s < steps; s += kGroupBatch) {
-    int t[kGroupBatch][4];
-    fetch(s, t);
+    uint32_t low[kGroupBatch][4], t[kGroupBatch][4];
+    fetch(s, low, t);
 #pragma unroll
-    for (int u = 0; u < kGroupBatch; ++u)
+    for (int u = 0; u < kGroupBatch; ++u) {
+      uint64_t met[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int low = t[u][j] >= 0 ? (t[u][j] & mask) : G;
-        less += low < g ? 1 : 0;
-        if (low == g) atomicAdd(&mine[t[u][j] >> a.shift], 1);
+        less += __popcll(__ballot(low[u][j] < g));
+        met[j] = __ballot(low[u][j] == g);
       }
+      if ((met[0] | met[1] | met[2] | met[3]) == 0) continue;
+      // the places of this step's owned rows among the notes: by lane, then
+      // by place in the lane
+      int at = noted;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        at += lanes_below(met[j]);
+        noted += __popcll(met[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (low[u][j] == g) {
+          atomicAdd(&mine[t[u][j] >> a.shift], 1);
+          if (at < kNotes) {
+            note_row[wave][at] = (uint32_t)(begin + (s + u) * 256 + lane * 4 + j);
+            note_key[wave][at] = (uint16_t)(t[u][j] >> a.shift);
+          }
+          ++at;
+        }
+    }
   }
-  for (int o = 32; o > 0; o >>= 1) less += __shfl_xor(less, o);
   if (lane == 0) lower[wave] = less;
   __syncthreads();
 
@@ -166,6 +203,7 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
   // by wave (at most one key a thread)
   int32_t total = 0;
   if (tid < keys) {
+#pragma unroll
     for (int w = 0; w < kGroupWaves; ++w) total += counts[w * keys + tid];
     totals[tid] = total;
   }
@@ -184,11 +222,14 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
   }
   if (g == G - 1 && tid == 0) *a.count = base + own;
   if (tid < keys) {
+    int32_t c[kGroupWaves];
+#pragma unroll
+    for (int w = 0; w < kGroupWaves; ++w) c[w] = counts[w * keys + tid];
     int32_t at = base + before - total;
+#pragma unroll
     for (int w = 0; w < kGroupWaves; ++w) {
-      const int32_t c = counts[w * keys + tid];
       counts[w * keys + tid] = at;
-      at += c;
+      at += c[w];
     }
   }
   // the gradient rows of owned tokens that the list does not hold
@@ -203,58 +244,75 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
     }
   }
   __syncthreads();
-  if (own == 0) return;
 
+  // One key of a group of up to 64 x P rows after another: `want` says which
+  // of a lane's P rows are in the group; their places are by lane, then by
+  // place in the lane.
+  auto write = [&](auto parts, uint64_t (&want)[decltype(parts)::value], const uint32_t (&key)[decltype(parts)::value],
+                   const uint32_t (&row)[decltype(parts)::value]) __attribute__((always_inline)) {
+    constexpr int P = decltype(parts)::value;
+    for (int turn = 0; turn < 64 * P; ++turn) {
+      uint64_t left = 0;
+#pragma unroll
+      for (int j = 0; j < P; ++j) left |= want[j];
+      if (left == 0) break;
+      uint32_t pick = key[P - 1];
+#pragma unroll
+      for (int j = P - 2; j >= 0; --j)
+        if ((want[j] >> lane) & 1u) pick = key[j];
+      const uint32_t now = (uint32_t)__builtin_amdgcn_readlane((int)pick, __builtin_ctzll(left));
+      uint64_t eq[P];
+      int below = 0, sum = 0;
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        eq[j] = __ballot(key[j] == now) & want[j];
+        want[j] &= ~eq[j];
+        below += lanes_below(eq[j]);
+        sum += __popcll(eq[j]);
+      }
+      int pos = mine[now] + below;
+#pragma unroll
+      for (int j = 0; j < P; ++j)
+        if ((eq[j] >> lane) & 1u) {
+          if (pos >= 0 && pos < a.n) {
+            a.rows[pos] = (int32_t)row[j];
+            a.grouped[pos] = (int32_t)((now << a.shift) + g);
+          }
+          ++pos;
+        }
+      // the wave's own counter: every lane has read it before lane 0 moves it
+      // on (the wave runs in step and its LDS operations stay in order); the
+      // fences keep the compiler from holding it in a register
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (lane == 0) mine[now] += sum;
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+  };
+  if (noted <= kNotes) {
+    for (int i = 0; i < noted; i += 64) {
+      const int at = i + lane < noted ? i + lane : i;
+      const uint32_t key[1] = {note_key[wave][at]}, row[1] = {note_row[wave][at]};
+      uint64_t want[1] = {__ballot(i + lane < noted)};
+      write(std::integral_constant<int, 1>(), want, key, row);
+    }
+    return;
+  }
   for (int64_t s = 0; s < steps; s += kGroupBatch) {
-    int batch[kGroupBatch][4];
-    fetch(s, batch);
+    uint32_t low[kGroupBatch][4], t[kGroupBatch][4];
+    fetch(s, low, t);
 #pragma unroll
     for (int u = 0; u < kGroupBatch; ++u) {
-      const int64_t at = begin + (s + u) * 256 + lane * 4;
-      int(&t)[4] = batch[u];
       uint64_t want[4];
+      uint32_t key[4], row[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) want[j] = __ballot(t[j] >= 0 && (t[j] & mask) == g);
-      // one token of this step after another: its rows' places are by lane,
-      // then by place in the lane
-      for (int turn = 0; turn < 256; ++turn) {  // at most 256 tokens
-        const uint64_t left = want[0] | want[1] | want[2] | want[3];
-        if (left == 0) break;
-        const int src = __builtin_ctzll(left);
-        int pick = t[3];
-#pragma unroll
-        for (int j = 2; j >= 0; --j)
-          if ((want[j] >> lane) & 1u) pick = t[j];
-        const int token = __builtin_amdgcn_readlane(pick, src);
-        uint64_t eq[4];
-        int below = 0, sum = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          eq[j] = __ballot(((want[j] >> lane) & 1u) && t[j] == token);
-          want[j] &= ~eq[j];
-          below += lanes_below(eq[j]);
-          sum += __popcll(eq[j]);
-        }
-        const int key = token >> a.shift;
-        int pos = mine[key] + below;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if ((eq[j] >> lane) & 1u) {
-            if (pos >= 0 && pos < a.n) {
-              a.rows[pos] = (int32_t)(at + j);
-              a.grouped[pos] = token;
-            }
-            ++pos;
-          }
-        // the wave's own counter: every lane has read it before lane 0 moves
-        // it on (the wave runs in step and its LDS operations stay in order);
-        // the fences keep the compiler from holding it in a register
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (lane == 0) mine[key] += sum;
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      for (int j = 0; j < 4; ++j) {
+        want[j] = __ballot(low[u][j] == g);
+        key[j] = t[u][j] >> a.shift;
+        row[j] = (uint32_t)(begin + (s + u) * 256 + lane * 4 + j);
       }
+      write(std::integral_constant<int, 4>(), want, key, row);
     }
   }
 }
@@ -264,7 +322,7 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
 struct RunArgs {
   const void* dy;
   int64_t n, dy_stride, vocab;
-  int hidden, span, lanes_shift;
+  int hidden, span, lanes_shift, tiles;
   const int32_t* rows;
   const int32_t* grouped;
   const int32_t* count;
@@ -298,31 +356,56 @@ constexpr int kSumSpots = 2048;  // grouped positions of a workgroup at most
 constexpr int kSumBatch = 8;     // rows a lane has in flight
 
 // A lane's N columns of a row.  The last lane of a row whose width is no
-// multiple of N takes the row's last N columns instead, so that every load is
-// a whole vector without a branch; the first `shift` of them belong to the
-// lane before and are not stored.  A width below N is loaded value by value,
-// the last one again in place of those past it.
+// multiple of N takes the row's last N columns instead, so that every load
+// and store is a whole vector without a branch: it sums the first `shift` of
+// them like the lane before it, to the same bits, and both store them.  Only
+// where a stored value depends on the one it replaces (adding to the
+// gradient) does it leave those out, since the lane before may be in another
+// workgroup.  A width below N is loaded value by value, the last one again in
+// place of those past it.
 template <typename T, int N, bool NARROW>
-__device__ __forceinline__ void load_columns(const T* p, int hidden, float (&v)[N]) {
-  if constexpr (NARROW) {
+struct Columns {
+  v4u raw[N / Type<T>::kVec];
+  __device__ __forceinline__ void load(const T* p, int hidden) {
+    constexpr int K = Type<T>::kVec;
+    if constexpr (NARROW) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = (float)p[i < hidden ? i : hidden - 1];
-  } else {
-    load_row<T, N>(p, N, v);
+      for (int j = 0; j < N / K; ++j) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const T x = p[min(j * K + i, hidden - 1)];
+          if constexpr (sizeof(T) == 4)
+            w[i] = __builtin_bit_cast(uint32_t, x);
+          else
+            w[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, x) << (16 * (i & 1));
+        }
+        raw[j] = v4u{w[0], w[1], w[2], w[3]};
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N / K; ++j) raw[j] = load_at<v4u, sizeof(T)>(p + j * K);
+    }
   }
-}
+  __device__ __forceinline__ void values(float (&v)[N]) const {
+    constexpr int K = Type<T>::kVec;
+#pragma unroll
+    for (int j = 0; j < N / K; ++j) {
+      float t[K];
+      widen<T>(raw[j], t);
+#pragma unroll
+      for (int i = 0; i < K; ++i) v[j * K + i] = t[i];
+    }
+  }
+};
 template <typename O, int N, bool NARROW>
-__device__ __forceinline__ void store_columns(O* p, const float (&v)[N], int shift, int hidden) {
+__device__ __forceinline__ void store_columns(O* p, const float (&v)[N], int hidden) {
   if constexpr (NARROW) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (i < hidden) p[i] = (O)v[i];
-  } else if (shift == 0) {
-    store_row<O, N>(p, v, N);
   } else {
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-      if (i >= shift) p[i] = (O)v[i];
+    store_row<O, N>(p, v, N);
   }
 }
 
@@ -340,10 +423,13 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
   __shared__ int32_t row[kSumSpots];
   __shared__ float heads[kSumThreads][N];
   const int tid = threadIdx.x;
+  // the tiles of a row next to each other: they are read at about one time
+  const int64_t block = blockIdx.x / a.tiles;
+  const int tile = (int)(blockIdx.x - block * a.tiles);
   const int lanes = 1 << a.lanes_shift, units = kSumThreads >> a.lanes_shift;
   const int unit = tid >> a.lanes_shift, lane = tid & (lanes - 1);
   const int spots = units * a.span;
-  const int64_t first = (int64_t)blockIdx.x * spots;
+  const int64_t first = (int64_t)block * spots;
   const int64_t m = listed_rows(a);
   if (first >= m) return;
   const int here = (int)(m - first < spots ? m - first : spots);
@@ -354,7 +440,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
   for (int i = tid; i < here; i += kSumThreads) row[i] = listed_row(a, first + i);
   __syncthreads();
 
-  const int want = (int)(blockIdx.y * lanes + lane) * N;
+  const int want = (int)(tile * lanes + lane) * N;
   const bool any = want < a.hidden;  // the other lanes repeat the last columns and store nothing
   const int col = NARROW ? 0 : min(want, a.hidden - N), shift = want - col;
   const T* dy = static_cast<const T*>(a.dy) + col;
@@ -372,24 +458,30 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = acc[i] * a.scale;
     if constexpr (ADD) {
+      Columns<O, N, NARROW> now;
+      now.load(p, a.hidden);
       float old[N];
-      load_columns<O, N, NARROW>(p, a.hidden, old);
+      now.values(old);
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += old[i];
     }
-    store_columns<O, N, NARROW>(p, v, shift, a.hidden);
+    if (ADD && !NARROW && shift > 0) {
+#pragma unroll
+      for (int i = 1; i < N; ++i)
+        if (i >= shift) p[i] = (O)v[i];
+    } else {
+      store_columns<O, N, NARROW>(p, v, a.hidden);
+    }
   };
   int token = num > 0 ? tok[1 + p0] : -1;
   bool ours = num > 0 && tok[p0] != token;  // this run begins in this row group
   bool head = false;                        // heads[tid] holds the end of a run begun before
+  // Positions past the last read the last row again and are dropped.
   for (int i0 = 0; i0 < num; i0 += kSumBatch) {
-    float v[kSumBatch][N];
-    // positions past the last read the batch's first row again and are dropped
+    Columns<T, N, NARROW> batch[kSumBatch];
 #pragma unroll
-    for (int u = 0; u < kSumBatch; ++u) {
-      const int i = i0 + u < num ? i0 + u : i0;
-      load_columns<T, N, NARROW>(dy + (int64_t)row[p0 + i] * a.dy_stride, a.hidden, v[u]);
-    }
+    for (int u = 0; u < kSumBatch; ++u)
+      batch[u].load(dy + (int64_t)row[p0 + min(i0 + u, num - 1)] * a.dy_stride, a.hidden);
 #pragma unroll
     for (int u = 0; u < kSumBatch; ++u) {
       if (i0 + u >= num) continue;
@@ -407,8 +499,10 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
         token = t;
         ours = true;
       }
+      float v[N];
+      batch[u].values(v);
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] += v[u][i];
+      for (int i = 0; i < N; ++i) acc[i] += v[i];
     }
   }
   if (num > 0 && !ours) {
@@ -421,7 +515,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
   if (num == 0) return;
   // collect the parts of later row groups: of this row group's last run, and
   // in row group 0 also of a run begun before the workgroup
-  const int64_t spot = (int64_t)blockIdx.x * a.pitch + col;
+  const int64_t spot = (int64_t)block * a.pitch + col;
   auto collect = [&](float (&sum)[N], int t) {
     for (int u = unit + 1; u < units; ++u) {
       if (u * a.span >= here || tok[1 + u * a.span] != t) break;
@@ -438,14 +532,14 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(RunArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) sum[i] = heads[tid][i];
     if (tok[min(a.span, here)] == t) (void)collect(sum, t);
-    if (any) store_columns<float, N, NARROW>(a.head + spot, sum, shift, a.hidden);
+    if (any) store_columns<float, N, NARROW>(a.head + spot, sum, a.hidden);
   }
   if (ours) {
     const bool on = collect(acc, token) && tok[here + 1] == token;
     if (!on)
       write(token);
     else if (any)
-      store_columns<float, N, NARROW>(a.tail + spot, acc, shift, a.hidden);
+      store_columns<float, N, NARROW>(a.tail + spot, acc, a.hidden);
   }
 }
 
@@ -590,15 +684,17 @@ hipError_t launch_embedding_grad(int dtype, const EmbeddingGradArgs& a, hipStrea
       using O = decltype(o);
       constexpr int N = Type<T>::kVec > Type<O>::kVec ? Type<T>::kVec : Type<O>::kVec;
       const unsigned tiles = (unsigned)ceil_div(a.hidden, (int64_t)l.lanes * N);
-      const dim3 grid((unsigned)l.blocks, tiles);
+      RunArgs b = s;
+      b.tiles = (int)tiles;
+      const unsigned grid = (unsigned)(l.blocks * tiles);
       if (a.hidden < N && a.accumulate)
-        sum_runs_kernel<T, O, true, true><<<grid, kSumThreads, 0, st>>>(s);
+        sum_runs_kernel<T, O, true, true><<<grid, kSumThreads, 0, st>>>(b);
       else if (a.hidden < N)
-        sum_runs_kernel<T, O, true, false><<<grid, kSumThreads, 0, st>>>(s);
+        sum_runs_kernel<T, O, true, false><<<grid, kSumThreads, 0, st>>>(b);
       else if (a.accumulate)
-        sum_runs_kernel<T, O, false, true><<<grid, kSumThreads, 0, st>>>(s);
+        sum_runs_kernel<T, O, false, true><<<grid, kSumThreads, 0, st>>>(b);
       else
-        sum_runs_kernel<T, O, false, false><<<grid, kSumThreads, 0, st>>>(s);
+        sum_runs_kernel<T, O, false, false><<<grid, kSumThreads, 0, st>>>(b);
       return hipGetLastError();
     });
   });
