@@ -349,9 +349,10 @@ def plain_norm_grad(dy, n, rstd, weight):
 
 
 def chain(rows, hidden):
-    """Rows that one wave or workgroup of the backward pass adds up."""
-    groups = 1024 * 4 if hidden <= 1024 else 1024 if hidden <= 4096 else 256
-    return -(-rows // groups) + 3
+    """Rows that one wave or workgroup of the backward pass adds up (at least
+    four, so that few partial sums are left), and the three other waves."""
+    groups = 512 * 4 if hidden <= 1024 else 512 if hidden <= 4096 else 128
+    return max(4, -(-rows // groups)) + 3
 
 
 @pytest.mark.parametrize("kept", [False, True], ids=["x", "kept"])
