@@ -33,9 +33,9 @@ def _code(dtype, name):
 def _on(t, name, dev=None):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
-    if dev is not None and t.device != dev:
+    if dev is not None and t.get_device() != dev.index:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
     return t
 
@@ -128,6 +128,11 @@ def _workspace(workspace, need, dev):
     return workspace
 
 
+def _fresh(t, dtype):
+    """A dense tensor of t's shape; empty_like is the cheapest way to one."""
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -163,9 +168,11 @@ def embedding(table, tokens, *, scale=1.0, dtype=None, out=None, stream=None):
     vocab, hidden, stride = _rows(table, "table")
     token_bytes = _tokens(tokens, dev)
     shape = (*tokens.shape, hidden)
+    out_stride = hidden
     if out is not None:
         dtype = out.dtype if dtype is None else dtype
         _like(out, "out", dev, shape, dtype)
+        out_stride = _rows(out, "out")[2]
     dtype = table.dtype if dtype is None else dtype
     codes = _code(table.dtype, "table"), _code(dtype, "out")
 
@@ -173,7 +180,7 @@ def embedding(table, tokens, *, scale=1.0, dtype=None, out=None, stream=None):
         y = torch.empty(shape, dtype=dtype, device=dev) if out is None else out
         _native.check(_native.lib().adasum_embedding(
             table.data_ptr(), vocab, hidden, stride, codes[0], tokens.data_ptr(), token_bytes, tokens.numel(),
-            scale, y.data_ptr(), _rows(y, "out")[2], codes[1], st))
+            scale, y.data_ptr(), out_stride, codes[1], st))
         return y
     return _call(dev, stream, body)
 
@@ -218,6 +225,7 @@ def embedding_grad(dy, tokens, vocab, *, scale=1.0, dtype=None, out=None, accumu
 def _norm(x, weight, bias, eps, out, stream, keep):
     dev = _on(x, "x").device
     rows, hidden, stride = _rows(x, "x")
+    out_stride = hidden
     code = _code(x.dtype, "x")
     param_code = 0
     if weight is not None:
@@ -229,20 +237,21 @@ def _norm(x, weight, bias, eps, out, stream, keep):
         param_code = bias_code
     if out is not None:
         _like(out, "out", dev, x.shape, x.dtype)
+        out_stride = _rows(out, "out")[2]
 
     def body(st):
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        y = _fresh(x, x.dtype) if out is None else out
         lead = x.shape[:-1]
         rstd = torch.empty(lead, dtype=torch.float32, device=dev)
         mean = codes = scales = None
         if keep:
-            codes = torch.empty(x.shape, dtype=torch.int8, device=dev)
+            codes = _fresh(x, torch.int8)
             scales = torch.empty((*lead, _blocks(hidden)), dtype=torch.uint8, device=dev)
         else:
             mean = torch.empty(lead, dtype=torch.float32, device=dev)
         _native.check(_native.lib().adasum_layer_norm(
             x.data_ptr(), rows, hidden, stride, code, _ptr(weight), _ptr(bias), param_code, eps, y.data_ptr(),
-            _rows(y, "out")[2], _ptr(mean), rstd.data_ptr(), _ptr(codes), _ptr(scales), st))
+            out_stride, _ptr(mean), rstd.data_ptr(), _ptr(codes), _ptr(scales), st))
         return (y, rstd, codes, scales) if keep else (y, mean, rstd)
     return _call(dev, stream, body)
 
@@ -278,8 +287,10 @@ def _norm_grad(dy, x, mean, codes, scales, rstd, weight, dx, dweight, dbias, acc
         raise ValueError("codes must have the width of dy")
     _dense(rstd, "rstd", dev, (rows,), torch.float32)
     param_code = _param(weight, "weight", dev, hidden) if weight is not None else 0
+    dx_stride = hidden
     if dx is not None:
         _like(dx, "dx", dev, dy.shape, dy.dtype)
+        dx_stride = _rows(dx, "dx")[2]
     if accumulate and (weight is None or dweight is None or dbias is None):
         raise ValueError("accumulate needs weight, dweight and dbias")
     grad_dtype = weight.dtype if weight is not None else torch.float32
@@ -301,14 +312,14 @@ def _norm_grad(dy, x, mean, codes, scales, rstd, weight, dx, dweight, dbias, acc
 
     def body(st):
         ws = _workspace(workspace, need, dev)
-        d = torch.empty(dy.shape, dtype=dy.dtype, device=dev) if dx is None else dx
+        d = _fresh(dy, dy.dtype) if dx is None else dx
         dw, db = dweight, dbias
         if weight is not None:
             dw = torch.empty(hidden, dtype=grad_dtype, device=dev) if dw is None else dw
             db = torch.empty(hidden, dtype=grad_dtype, device=dev) if db is None else db
         _native.check(L.adasum_layer_norm_grad(
             dy.data_ptr(), rows, hidden, stride, code, _ptr(x), x_stride, _ptr(mean), _ptr(codes), _ptr(scales),
-            rstd.data_ptr(), _ptr(weight), param_code, d.data_ptr(), _rows(d, "dx")[2], _ptr(dw), _ptr(db), grad_code,
+            rstd.data_ptr(), _ptr(weight), param_code, d.data_ptr(), dx_stride, _ptr(dw), _ptr(db), grad_code,
             int(accumulate), _ptr(ws), _size(ws), st))
         return d, dw, db
     return _call(dev, stream, body)
@@ -353,7 +364,7 @@ def checkpoint_pack(x, *, codes=None, scales=None, stream=None):
         _dense(scales, "scales", dev, shape, torch.uint8)
 
     def body(st):
-        c = torch.empty(x.shape, dtype=torch.int8, device=dev) if codes is None else codes
+        c = _fresh(x, torch.int8) if codes is None else codes
         s = torch.empty(shape, dtype=torch.uint8, device=dev) if scales is None else scales
         _native.check(_native.lib().adasum_checkpoint_pack(x.data_ptr(), rows, width, stride, code, c.data_ptr(),
                                                            s.data_ptr(), st))
@@ -366,13 +377,15 @@ def checkpoint_unpack(codes, scales, dtype=torch.float32, *, out=None, stream=No
     dev = _on(codes, "codes").device
     rows, width = _packed(codes, scales, dev, None, "")
     code = _code(dtype, "dtype")
+    out_stride = width
     if out is not None:
         _like(out, "out", dev, codes.shape, dtype)
+        out_stride = _rows(out, "out")[2]
 
     def body(st):
-        y = torch.empty(codes.shape, dtype=dtype, device=dev) if out is None else out
+        y = _fresh(codes, dtype) if out is None else out
         _native.check(_native.lib().adasum_checkpoint_unpack(codes.data_ptr(), scales.data_ptr(), rows, width,
-                                                             y.data_ptr(), _rows(y, "out")[2], code, st))
+                                                             y.data_ptr(), out_stride, code, st))
         return y
     return _call(dev, stream, body)
 
