@@ -203,8 +203,8 @@ __device__ __forceinline__ float wave_sum(float x) {
 // 32 consecutive values of a row share one power of two 2^e, stored as the
 // byte e + 127; a value is code * 2^e with a signed 8-bit code.  e is the
 // least exponent with 127 * 2^e >= the block's largest magnitude, so no code
-// is clipped, and a code is off by at most half a step: 2^(e-1), below 1/126
-// of the block's largest magnitude.  Scaling by a power of two is exact, so
+// is clipped, and a code is off by at most half a step: 2^(e-1), 1/127 of
+// the block's largest magnitude.  Scaling by a power of two is exact, so
 // the only rounding is that of the code.  Byte 255 marks a block that held an
 // infinity or NaN: all of it reads back as NaN.
 

@@ -116,8 +116,8 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_kernel(NormArgs a)
     row_sum<LPR, 2>(s2, lds2, slot);
     slot ^= 1;
     const float rest = s2[0] * inv_h;
-    const float var = fmaxf(__builtin_fmaf(-rest, rest, s2[1] * inv_h), 0.f);
-    const float rstd = inverse_root(var + a.eps);
+    const float var = __builtin_fmaf(-rest, rest, s2[1] * inv_h);
+    const float rstd = inverse_root((var < 0.f ? 0.f : var) + a.eps);  // NaN where the row holds one, or an infinity
     if (lane == 0) {
       if (a.mean) a.mean[r] = m + rest;
       a.rstd[r] = rstd;
@@ -312,9 +312,8 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t st) {
 struct GradShape {
   int lanes, threads, rows;
 };
-GradShape grad_shape(int dtype, int hidden) {
+GradShape grad_shape(int hidden) {
   const int per_wave = 64 * 16;
-  (void)dtype;
   if (hidden <= per_wave) return {64, 256, 4};
   if (hidden <= 4 * per_wave) return {256, 256, 1};
   return {1024, 1024, 1};
@@ -361,8 +360,8 @@ hipError_t launch_norm(int dtype, const NormArgs& a, hipStream_t st) {
   return with_dtype(dtype, [&](auto t) { return norm_width<decltype(t)>(a, st); });
 }
 
-int norm_grad_blocks(int dtype, int64_t rows, int hidden) {
-  const GradShape s = grad_shape(dtype, hidden);
+int norm_grad_blocks(int64_t rows, int hidden) {
+  const GradShape s = grad_shape(hidden);
   // Two workgroups of 256 lanes per CU, or as many waves in wider ones, and
   // no more than leaves each four rows a wave: every workgroup leaves a row of
   // partial sums for the join.  65536 x 1024 bf16: 75 us whether 512 or 1024
@@ -371,8 +370,8 @@ int norm_grad_blocks(int dtype, int64_t rows, int hidden) {
 }
 
 hipError_t launch_norm_grad(int dtype, const NormGradArgs& a, hipStream_t st) {
-  const GradShape s = grad_shape(dtype, a.hidden);
-  const int blocks = a.rows > 0 ? norm_grad_blocks(dtype, a.rows, a.hidden) : 0;
+  const GradShape s = grad_shape(a.hidden);
+  const int blocks = a.rows > 0 ? norm_grad_blocks(a.rows, a.hidden) : 0;
   if (blocks > 0) {
     const hipError_t e =
         with_dtype(dtype, [&](auto t) { return norm_grad_width<decltype(t)>(a, s.lanes, blocks, st); });

@@ -17,6 +17,10 @@ constexpr int kCUs = 256;                 // compute units of an MI355X
 constexpr int kScaleBlock = 32;           // values that share an 8-bit scale
 constexpr int kMaxNormHidden = 16384;     // widest row of the layer norm kernels (held in registers)
 constexpr int64_t kMaxDim = int64_t(1) << 31;  // rows, tokens, vocabulary and widths stay below this
+constexpr int64_t kMaxEmbeddingHidden = int64_t(1) << 23;  // a launch has 65536 workgroups along a row at most
+// Row stride of the linear gradient's dy: eight rows' offsets are taken in 32
+// bits (in 64 bits the kernel's loads cost it 1 to 2 % of its time).
+constexpr int64_t kMaxLinearStride = int64_t(1) << 28;
 
 // f(value of the C++ type of a dtype code), for picking a kernel.
 template <typename F>
@@ -67,7 +71,7 @@ struct NormGradArgs {
   float* partials;      // norm_grad_blocks(...) x 2 x hidden
 };
 // Workgroups of the backward pass, each with a row of partial sums.
-int norm_grad_blocks(int dtype, int64_t rows, int hidden);
+int norm_grad_blocks(int64_t rows, int hidden);
 hipError_t launch_norm_grad(int dtype, const NormGradArgs& a, hipStream_t st);
 
 // ---------------------------------------------------------------- 8-bit activations

@@ -113,6 +113,8 @@ auto guarded(F f) -> decltype(f()) {
     return fail(ADASUM_ENOMEM, "out of host memory");
   } catch (const std::exception& e) {
     return fail(ADASUM_EHIP, e.what());
+  } catch (...) {
+    return fail(ADASUM_EHIP, "unknown exception");
   }
 }
 
@@ -128,6 +130,7 @@ int embedding(const void* table, int64_t vocab, int64_t hidden, int64_t table_st
   size_t table_bytes = 0, out_bytes = 0;
   RETURN_IF(check_matrix(vocab, hidden, table_stride, table_dtype, "table", &table_bytes));
   RETURN_IF(check_matrix(n, hidden, out_stride, out_dtype, "out", &out_bytes));
+  if (hidden > kMaxEmbeddingHidden) return fail(ADASUM_EINVAL, "embedding: hidden must be at most 2^23");
   if (vocab < 1 || vocab > kMaxVocab) return fail(ADASUM_EINVAL, "vocab must be in [1, 2^24]");
   if (token_bytes != 4 && token_bytes != 8) return fail(ADASUM_EINVAL, "token_bytes must be 4 or 8");
   if (!std::isfinite((float)scale)) return fail(ADASUM_EINVAL, "scale must be finite in fp32");
@@ -155,6 +158,7 @@ int embedding(const void* table, int64_t vocab, int64_t hidden, int64_t table_st
 int64_t embedding_grad_bytes(int64_t n, int64_t hidden, int dtype) {
   size_t bytes = 0;
   RETURN_IF(check_matrix(n, hidden, hidden, dtype, "dy", &bytes));
+  if (hidden > kMaxEmbeddingHidden) return fail(ADASUM_EINVAL, "embedding: hidden must be at most 2^23");
   return (int64_t)embedding_grad_layout(n, (int)hidden, dtype).total;
 }
 
@@ -164,6 +168,7 @@ int embedding_grad(const void* dy, int64_t n, int64_t hidden, int64_t dy_stride,
   size_t dy_bytes = 0, grad_bytes = 0;
   RETURN_IF(check_matrix(n, hidden, dy_stride, dtype, "dy", &dy_bytes));
   RETURN_IF(check_matrix(vocab, hidden, hidden, grad_dtype, "grad", &grad_bytes));
+  if (hidden > kMaxEmbeddingHidden) return fail(ADASUM_EINVAL, "embedding: hidden must be at most 2^23");
   if (vocab < 1 || vocab > kMaxVocab) return fail(ADASUM_EINVAL, "vocab must be in [1, 2^24]");
   if (token_bytes != 4 && token_bytes != 8) return fail(ADASUM_EINVAL, "token_bytes must be 4 or 8");
   if (!std::isfinite((float)scale)) return fail(ADASUM_EINVAL, "scale must be finite in fp32");
@@ -235,15 +240,15 @@ int layer_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, in
   return launch(kNorm, "layer norm", bytes, st, [&] { return launch_norm(dtype, a, st); });
 }
 
-size_t norm_grad_workspace(int64_t rows, int64_t hidden, int dtype) {
-  return rows == 0 ? 0 : (size_t)norm_grad_blocks(dtype, rows, (int)hidden) * 2 * hidden * sizeof(float);
+size_t norm_grad_workspace(int64_t rows, int64_t hidden) {
+  return rows == 0 ? 0 : (size_t)norm_grad_blocks(rows, (int)hidden) * 2 * hidden * sizeof(float);
 }
 
 int64_t layer_norm_grad_bytes(int64_t rows, int64_t hidden, int dtype) {
   size_t bytes = 0;
   RETURN_IF(check_matrix(rows, hidden, hidden, dtype, "dy", &bytes));
   if (hidden > kMaxNormHidden) return fail(ADASUM_EINVAL, "layer norm: hidden must be at most 16384");
-  return (int64_t)norm_grad_workspace(rows, hidden, dtype);
+  return (int64_t)norm_grad_workspace(rows, hidden);
 }
 
 int layer_norm_grad(const void* dy, int64_t rows, int64_t hidden, int64_t dy_stride, int dtype, const void* x,
@@ -267,7 +272,7 @@ int layer_norm_grad(const void* dy, int64_t rows, int64_t hidden, int64_t dy_str
   }
   const bool sums = dweight != nullptr || dbias != nullptr;
   if (rows == 0 && (accumulate || !sums)) return ADASUM_OK;
-  const size_t need = sums ? norm_grad_workspace(rows, hidden, dtype) : 0;
+  const size_t need = sums ? norm_grad_workspace(rows, hidden) : 0;
   RETURN_IF(check_workspace(workspace, workspace_bytes, need));
   const size_t param = (size_t)hidden * size_of(param_dtype), grad = (size_t)hidden * size_of(grad_dtype);
   const size_t stat = (size_t)rows * 4;
@@ -355,6 +360,8 @@ int check_linear(int64_t rows, int64_t out, int64_t in, int64_t stride, int dtyp
   RETURN_IF(check_matrix(rows, out, stride, dtype, "dy", dy_bytes));
   if (in < 1 || in > kMaxVocab || out > kMaxVocab)
     return fail(ADASUM_EINVAL, "in_features and out_features must be in [1, 2^24]");
+  if (rows > 1 && stride > kMaxLinearStride)
+    return fail(ADASUM_EINVAL, "linear gradient: the row stride of dy must be at most 2^28 elements");
   if (in > kMaxElements / out || (rows > 0 && in > kMaxElements / rows))
     return fail(ADASUM_EINVAL, "linear gradient: over 2^40 elements");
   const LinearGradLayout l = linear_grad_layout(rows, out, in, dtype);

@@ -241,7 +241,8 @@ ADASUM_API int64_t adasum_sum_workspace_bytes(int K, int64_t N, int dtype);
  * [0, vocab): such a token is no token (padding, or a row that another
  * worker's part of the table holds).
  *
- *   table        vocab rows of hidden elements of table_dtype, vocab <= 2^24.
+ *   table        vocab rows of hidden elements of table_dtype, vocab <= 2^24,
+ *                hidden <= 2^23.
  *   tokens       n indices of token_bytes (4 or 8: int32 or int64) each.
  *   scale        finite in fp32.
  *   out          n rows of hidden elements of out_dtype.
@@ -257,7 +258,7 @@ ADASUM_API int adasum_embedding(const void* table, int64_t vocab, int64_t hidden
  * accumulating).  Rows of dy whose token is none are not read.  The rows of a
  * token are summed in a fixed order, without atomics on the sums.
  *
- *   dy           n rows of hidden elements of dtype.
+ *   dy           n rows of hidden elements of dtype, hidden <= 2^23.
  *   grad         dense, vocab x hidden elements of grad_dtype.
  *   workspace    adasum_embedding_grad_workspace_bytes(n, hidden, dtype) bytes.
  */
@@ -336,7 +337,8 @@ ADASUM_API int adasum_checkpoint_unpack(const int8_t* codes, const uint8_t* scal
  * dbias[o] = sum over rows of dy[r][o].  Products are exact.  in_features and
  * out_features are at most 2^24.
  *
- *   dy           rows x out_features elements of dtype.
+ *   dy           rows x out_features elements of dtype; dy_stride <= 2^28
+ *                (of two rows or more).
  *   codes, scales rows x in_features activations packed from dtype (fp16:
  *                their values must be fp16 values, as packed ones are).
  *   dweight      dense, out_features x in_features elements of grad_dtype.

@@ -336,6 +336,33 @@ def test_layer_norm_hard_rows(gpu):
     assert bool(y[6:8].isnan().all())
 
 
+def test_layer_norm_statistics_of_bad_rows(gpu):
+    """A row with an infinity or NaN has NaN statistics, kept rows read NaN,
+    and neither the rows beside it nor their gradients notice; dweight and
+    dbias do."""
+    for dtype in DTYPES:
+        for hidden in (40, 1000, 5000):
+            x, w, dy = randn(30, 9, hidden, dtype=dtype), randn(31, hidden), randn(32, 9, hidden, dtype=dtype)
+            bad = x.clone()
+            bad[2, hidden - 1], bad[5, 0], bad[8] = float("inf"), float("nan"), float("-inf")
+            keep = [0, 1, 3, 4, 6, 7]
+            good, got = A.layer_norm(x, w), A.layer_norm(bad, w)
+            for a, b in zip(good, got, strict=True):
+                assert torch.equal(a[keep], b[keep])
+            for i in (2, 5, 8):
+                assert bool(got[0][i].isnan().all()) and bool(got[2][i].isnan())
+            y, rstd, codes, scales = A.layer_norm_keep(bad, w)
+            assert torch.equal(y[keep], good[0][keep]) and torch.equal(rstd[keep], good[2][keep])
+            assert bool(A.checkpoint_unpack(codes, scales)[[2, 5, 8]].isnan().all())
+            dx, dw, db = A.layer_norm_grad(dy, bad, *got[1:], w)
+            ref = A.layer_norm_grad(dy, x, *good[1:], w)
+            assert torch.equal(dx[keep], ref[0][keep]) and bool(dx[[2, 5, 8]].isnan().all())
+            assert bool(dw.isnan().all()) and torch.equal(db, ref[2])
+            kx, kw, kb = A.layer_norm_keep_grad(dy, codes, scales, rstd, w)
+            assert bool(kx[[2, 5, 8]].isnan().all()) and bool(torch.isfinite(kx[keep]).all())
+            assert bool(kw.isnan().all()) and torch.equal(kb, ref[2])
+
+
 def plain_norm_grad(dy, n, rstd, weight):
     dy, n, r = dy.double(), n.double(), rstd.double()[..., None]
     g = dy if weight is None else dy * weight.double()
@@ -859,6 +886,48 @@ def test_offsets_past_32_bits(gpu):
     x.zero_()
     A.layer_norm(near, w, out=x)
     assert torch.equal(x, close[0])
+
+
+def test_sizes_at_the_limits(gpu):
+    """The largest vocabularies, widths and strides that a call takes."""
+    flush_print("vocab 131072 and 2^24")
+    for vocab, hidden in ((131072, 8), (131073, 3), (1 << 24, 1)):
+        tok, dy = tokens_of(163, 3000, vocab, "uniform"), randn(164, 3000, hidden)
+        tok[:3] = torch.tensor([0, vocab - 1, vocab], device="cuda")
+        ref, mag = plain_embedding_grad(dy, tok, vocab, 1.0)
+        within(A.embedding_grad(dy, tok, vocab), ref, ref.abs() * 3 * E + mag * 544 * E, "gradient")
+    flush_print("hidden 2^23")
+    tok = torch.tensor([1, 0, 1, 2], device="cuda")
+    dy = torch.arange(4 << 23, device="cuda", dtype=F32).view(4, 1 << 23).remainder_(8191)
+    got = A.embedding_grad(dy, tok, 3)
+    assert torch.equal(got[0], dy[1]) and torch.equal(got[1], dy[0] + dy[2]) and torch.equal(got[2], dy[3])
+    assert torch.equal(A.embedding(dy, tok, scale=0.5), dy[tok] * 0.5)
+    flush_print("width 10000019")
+    x = dy.view(-1)[:20000038].view(2, 10000019)
+    codes, scales = A.checkpoint_pack(x)
+    for r in range(2):
+        c, s = A.checkpoint_pack(x[r, 9999968:])  # from a block's beginning
+        assert torch.equal(codes[r, 9999968:], c) and torch.equal(scales[r, 312499:], s)
+    del got, dy, x
+    flush_print("out_features and in_features 2^24")
+    dz, (codes, scales) = randn(165, 3, 1 << 24, dtype=BF16), A.checkpoint_pack(randn(166, 3, 2, dtype=BF16))
+    want = dz.double().t() @ A.checkpoint_unpack(codes, scales).double()
+    dw, db = A.linear_grad(dz, codes, scales, dtype=F32)
+    assert float((dw - want).abs().max()) <= 3 * 2.0 ** -23 * float(dz.abs().max()) * 8 * 3
+    assert float((db - dz.double().sum(0)).abs().max()) <= 2 * E * 3 * float(dz.abs().max())
+    codes, scales = A.checkpoint_pack(dz)
+    dw, _ = A.linear_grad(dz[:, :2].contiguous(), codes, scales, dtype=F32)
+    want = dz[:, :2].double().t() @ A.checkpoint_unpack(codes, scales).double()
+    assert float((dw - want).abs().max()) <= 3 * 2.0 ** -23 * float(dz.abs().max()) ** 2 * 3 * 1.01
+    del dz, dw, db, want, codes, scales
+    flush_print("row stride 2^28")
+    big = torch.empty(8 * (1 << 28) + 70, dtype=BF16, device="cuda")
+    x = big.as_strided((9, 70), (1 << 28, 1))
+    x.copy_(randn(167, 9, 70, dtype=BF16))
+    packed = A.checkpoint_pack(randn(168, 9, 300, dtype=BF16))
+    assert same(A.linear_grad(x, *packed, dtype=F32), A.linear_grad(x.contiguous(), *packed, dtype=F32))
+    with pytest.raises(A.AdasumError, match="2\\^28"):
+        A.linear_grad(big.as_strided((8, 70), ((1 << 28) + 1, 1)), *A.checkpoint_pack(randn(168, 8, 300, dtype=BF16)))
 
 
 def test_workers_gradients_into_the_combine(gpu):

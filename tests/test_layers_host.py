@@ -52,6 +52,8 @@ BAD = [
     ("adasum_embedding", dict(hidden=0), "width"),
     ("adasum_embedding", dict(hidden=-1), "width"),
     ("adasum_embedding", dict(table_stride=63), "stride"),
+    ("adasum_embedding", dict(hidden=(1 << 23) + 1, table_stride=1 << 24, out_stride=1 << 24), "2^23"),
+    ("adasum_embedding_grad", dict(hidden=(1 << 23) + 1, dy_stride=1 << 24), "2^23"),
     ("adasum_embedding", dict(out_stride=63), "stride"),
     ("adasum_embedding", dict(n=-1), "rows"),
     ("adasum_embedding", dict(n=1 << 31), "rows"),
@@ -118,6 +120,7 @@ BAD = [
     ("adasum_checkpoint_unpack", dict(out=None), "out is NULL"),
     ("adasum_checkpoint_unpack", dict(out=at(1) - 4), "overlaps"),
     ("adasum_checkpoint_unpack", dict(dtype=9), "dtype"),
+    ("adasum_linear_grad", dict(dy_stride=(1 << 28) + 1), "2^28"),
     ("adasum_linear_grad", dict(dy=None), "dy is NULL"),
     ("adasum_linear_grad", dict(dweight=None), "dweight is NULL"),
     ("adasum_linear_grad", dict(in_=0), "in_features"),
