@@ -18,8 +18,8 @@ constexpr int kScaleBlock = 32;           // values that share an 8-bit scale
 constexpr int kMaxNormHidden = 16384;     // widest row of the layer norm kernels (held in registers)
 constexpr int64_t kMaxDim = int64_t(1) << 31;  // rows, tokens, vocabulary and widths stay below this
 constexpr int64_t kMaxEmbeddingHidden = int64_t(1) << 23;  // a launch has 65536 workgroups along a row at most
-// Row stride of the linear gradient's dy: eight rows' offsets are taken in 32
-// bits (in 64 bits the kernel's loads cost it 1 to 2 % of its time).
+// Row stride of the linear gradient's dy: a row's offset is the product of two
+// 32-bit numbers, the row and the stride in bytes.
 constexpr int64_t kMaxLinearStride = int64_t(1) << 28;
 
 // f(value of the C++ type of a dtype code), for picking a kernel.

@@ -6,9 +6,9 @@
 //
 // on the matrix cores.  The sum runs over the slow axis of both operands, the
 // rows, while a matrix instruction takes eight consecutive terms of the sum
-// per lane.  So a thread loads the same few columns of eight rows and turns
-// the 8 x 4 patch while it writes it to LDS, where a column's rows are then
-// consecutive.
+// per lane.  So rows are staged in LDS as they lie in memory, as 16-bit
+// values, and turned by the transposing LDS reads, which give a lane four
+// rows of its column.
 //
 // Products are exact: a code times a power of two has 7 significant bits and
 // is a bf16 value, and an fp16 value too where fp16 activations were packed.
@@ -35,15 +35,16 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 // A workgroup of eight waves takes 256 columns of x by kTileY of dy and walks
 // the rows 32 at a time; a wave holds 64 x kWaveY sums.  16-bit dy: 256 x 256
 // outputs, 128 sums a lane.  fp32 dy, with three times the matrix
-// instructions and LDS per column: half as many columns of dy.
-constexpr int kStep = 32, kChunks = kStep / 8, kThreads = 512, kTileX = 256, kWaveX = 64, kColsX = 4;
+// instructions and LDS per column: half as many columns of dy.  A thread
+// stages kVecX codes of each of two rows, or kVecY values of dy of kRowsY.
+constexpr int kStep = 32, kThreads = 512, kTileX = 256, kWaveX = 64, kVecX = 16, kRowsX = 2, kVecY = 8;
 template <typename T>
 struct Shape {
-  static constexpr int kParts = 1, kTileY = 256, kWaveY = 128, kColsY = 4;
+  static constexpr int kParts = 1, kTileY = 256, kWaveY = 128;
 };
 template <>
 struct Shape<float> {
-  static constexpr int kParts = 3, kTileY = 128, kWaveY = 64, kColsY = 2;
+  static constexpr int kParts = 3, kTileY = 128, kWaveY = 64;
 };
 constexpr int kAhead = 2;  // steps whose loads are in flight, and buffers in LDS
 
@@ -73,120 +74,150 @@ __device__ __forceinline__ void cut3(float v, uint32_t (&part)[3]) {
 __device__ __forceinline__ uint32_t upper_pair(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
-__device__ __forceinline__ uint32_t lower_pair(uint32_t a, uint32_t b) {
-  return __builtin_amdgcn_perm(b, a, 0x05040100u);
+
+// LDS holds a step's rows of `cols` 16-bit values each, as segments of 16
+// columns that are permuted within the row by the row's number: a transposing
+// read takes the same segment of 16 rows, which would otherwise lie in the
+// same eight banks.
+__device__ __forceinline__ int segment_key(int row) { return (row & 3) | ((row >> 1) & 4); }
+// 16-byte piece `piece` (eight columns) of a row, in units of 16 bytes
+__device__ __forceinline__ int piece_at(int row, int piece, int cols) {
+  return row * (cols / 8) + (piece ^ (segment_key(row) * 2));
 }
 
-// LDS holds a column's 32 rows as four 16-byte chunks of eight.  Every four
-// columns are a 256-byte line, whose 16 chunks are permuted by the line's
-// number: then neither the 16 neighbouring columns that a matrix
-// instruction's lanes read, nor the columns that neighbouring threads write
-// (every second or fourth), meet in a bank.
-__device__ __forceinline__ int chunk_at(int col, int chunk) { return (col * 4 + chunk) ^ ((col >> 2) & 15); }
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+// Eight rows of a lane's column: lane i of 16 names four columns of row i / 4,
+// and gets column i of the four rows; `at` is the byte address for the first
+// four of the eight rows, `pitch` a row's bytes.
+__device__ __forceinline__ v4u turned(const v4u* base, uint32_t at, int pitch) {
+  const char* p = reinterpret_cast<const char*>(base) + at;
+  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p));
+  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)(p + 4 * pitch));
+  return __builtin_bit_cast(v4u, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Four words moved down by `bits` below 128.
+__device__ __forceinline__ void shift_down(uint32_t* w, int bits) {
+  const uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
+  const int b = bits & 63;
+  const uint64_t both = (lo >> b) | ((hi << 1) << (63 - b));
+  const uint64_t l = bits >= 64 ? hi >> b : both, h = bits >= 64 ? 0u : hi >> b;
+  w[0] = (uint32_t)l;
+  w[1] = (uint32_t)(l >> 32);
+  w[2] = (uint32_t)h;
+  w[3] = (uint32_t)(h >> 32);
+}
 
 // The first four waves load and stage x, the other four dy, each thread the
-// same few columns of eight rows; all eight run the matrix instructions.  In
-// step t a wave computes on one LDS buffer while it stages step t + 1 into
-// the next and then asks for step t + 1 + kAhead: one barrier a step, and
-// kAhead steps of loads on their way.
+// same columns of its rows; all eight run the matrix instructions.  In step t
+// a wave computes on one LDS buffer while it stages step t + 1 into the next
+// and then asks for step t + 1 + kAhead: one barrier a step, and kAhead steps
+// of loads on their way.
 template <typename T, bool NARROW>
 __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs a, LinearGradLayout l) {
   using S = Shape<T>;
-  constexpr int P = S::kParts, CX = kColsX, CY = S::kColsY;
+  constexpr int P = S::kParts, TY = S::kTileY;
   constexpr int MX = kWaveX / 16, NY = S::kWaveY / 16, WAVES_X = kTileX / kWaveX;
-  static_assert(CY * sizeof(T) == 8, "a row of a thread's columns of dy is two words");
-  __shared__ v4u lds_x[kAhead][kTileX * kChunks];
-  __shared__ v4u lds_y[kAhead][P][S::kTileY * kChunks];
+  // four waves, each with 64 / (columns / a lane's) rows at a time
+  constexpr int LANES_X = kTileX / kVecX, LANES_Y = TY / kVecY;  // lanes of a row
+  constexpr int PASS_X = 4 * 64 / LANES_X, PASS_Y = 4 * 64 / LANES_Y, ROWS_Y = kStep / PASS_Y;
+  static_assert(PASS_X * kRowsX == kStep && ROWS_Y * kVecY * sizeof(T) == 64, "16 words a thread and step");
+  __shared__ v4u lds_x[kAhead][kStep * kTileX / 8];
+  __shared__ v4u lds_y[kAhead][P][kStep * TY / 8];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
 
   const int64_t tiles = l.tiles_out * l.tiles_in;
   const int64_t split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
   const int64_t tile_o = tile / l.tiles_in, tile_i = tile - tile_o * l.tiles_in;
-  const int64_t o0 = tile_o * S::kTileY, i0 = tile_i * kTileX;
+  const int64_t o0 = tile_o * TY, i0 = tile_i * kTileX;
   const int64_t r_begin = split * l.split_rows;
   const int rows = (int)std::max<int64_t>(0, std::min(l.split_rows, a.rows - r_begin));  // of this split
   const int64_t nb = (a.in + kScaleBlock - 1) / kScaleBlock;
   const int steps = (rows + kStep - 1) / kStep;
 
-  // This thread's patch: rows 8 k .. 8 k + 7 of columns c .. of x or of dy.
-  // Past the edge any column will do, since its sums are not stored; a patch
-  // across the edge loads the last whole patch of the row and moves it down
-  // by `shift` bits.  (A matrix narrower than a patch is loaded value by
-  // value.)
+  // This thread's columns c .. of x or of dy, of the step's rows my_row +
+  // PASS u.  Past the edge any column will do, since its sums are not stored;
+  // columns across the edge are loaded as the last whole vector of the row
+  // and moved down by `shift` bits.  (A matrix narrower than a vector is
+  // loaded value by value.)
   const bool is_x = wave < 4;
-  const int k = wave & 3;
-  const int c = lane * (is_x ? CX : CY);
+  const int in_row = lane & ((is_x ? LANES_X : LANES_Y) - 1);
+  const int my_row = ((wave & 3) * 64 + lane) / (is_x ? LANES_X : LANES_Y);
+  const int cols = is_x ? kVecX : kVecY, c = in_row * cols;
   const int64_t width = is_x ? a.in : a.out, col = (is_x ? i0 : o0) + c;
-  const int cols = is_x ? CX : CY;
   const int64_t from = col + cols <= width ? col : width - cols;
   const int shift = !NARROW && col < width && col > from ? (int)(col - from) * (is_x ? 8 : 8 * (int)sizeof(T)) : 0;
   const bool shifts = __ballot(shift != 0) != 0;
 
-  // x: eight rows of codes and one scale byte, of row lane / 8 and block
-  // lane % 8 of the wave's eight rows; dy: eight rows of two words
-  uint32_t set[kAhead][16];
+  // x: two rows of 16 codes, and their scale bytes in `byte`; dy: 64 bytes of
+  // ROWS_Y rows
+  uint32_t set[kAhead][16], byte[kAhead][kRowsX];
 
-  // Step t's loads.  A wave's rows are the same for all its lanes: row
-  // pointers are scalars, and a lane adds one 32-bit offset, the same for
-  // every row.  There is no branch around the loads (steps and rows past the
+  // Step t's loads.  There is no branch around them (steps and rows past the
   // split's end read its last row; trim clears dy's), so that the waits for a
-  // step's loads leave the later steps' on their way.
-  const uint32_t off0 = (uint32_t)((NARROW ? 0 : from) * (is_x ? 1 : (int64_t)sizeof(T)));
-  const uint32_t block = (uint32_t)std::min<int64_t>(i0 / kScaleBlock + (lane & 7), nb - 1);
-  auto read = [&](auto x_wave, uint32_t (&w)[16], int t) __attribute__((always_inline)) {
-    const int first = std::min(t * kStep + 8 * k, rows - 1), left = rows - 1 - first;
-    uint32_t off = off0;
-    asm("" : "+v"(off));  // opaque here, so that the address is a scalar and this offset
+  // step's loads leave the later steps' on their way.  A row's offset is 32 x
+  // 32 bits.
+  const char* const base = is_x ? reinterpret_cast<const char*>(a.codes + r_begin * a.in + (NARROW ? 0 : from))
+                                : reinterpret_cast<const char*>(static_cast<const T*>(a.dy) + r_begin * a.dy_stride +
+                                                                (NARROW ? 0 : from));
+  const uint8_t* const scale_base = a.scales + r_begin * nb + std::min<int64_t>(col / kScaleBlock, nb - 1);
+  const uint32_t pitch = is_x ? (uint32_t)a.in : (uint32_t)(a.dy_stride * sizeof(T));
+  auto read = [&](auto x_wave, uint32_t (&w)[16], uint32_t (&b)[kRowsX], int t) __attribute__((always_inline)) {
     if constexpr (decltype(x_wave)::value) {
-      const int8_t* x0 = a.codes + (r_begin + first) * a.in;
-      const uint8_t* s0 = a.scales + (r_begin + first) * nb;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int row = std::min(e, left);
-        const int8_t* x = x0 + row * (int)a.in;
+      for (int u = 0; u < kRowsX; ++u) {
+        const uint32_t row = (uint32_t)std::min(t * kStep + PASS_X * u + my_row, rows - 1);
+        const char* x = base + (uint64_t)row * pitch;
         if constexpr (NARROW) {
-          w[e] = 0u;
 #pragma unroll
-          for (int q = 0; q < CX; ++q)
-            w[e] |= (uint32_t)(uint8_t)x[std::min<int64_t>(col + q, width - 1)] << (8 * q);
+          for (int i = 0; i < 4; ++i) w[4 * u + i] = 0u;
+#pragma unroll
+          for (int i = 0; i < kVecX; ++i)
+            w[4 * u + i / 4] |= (uint32_t)(uint8_t)x[std::min<int64_t>(col + i, width - 1)] << (8 * (i & 3));
         } else {
-          w[e] = load_at<uint32_t, 1>(x + off);
+          const v4u v = load_at<v4u, 1>(x);
+          w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
         }
+        b[u] = scale_base[(uint64_t)row * (uint32_t)nb];
       }
-      w[8] = s0[(uint32_t)(std::min(lane >> 3, left) * (int)nb) + block];
     } else {
-      const T* y0 = static_cast<const T*>(a.dy) + (r_begin + first) * a.dy_stride;
+      constexpr int W = 16 / ROWS_Y;  // words of a row
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const T* y = y0 + std::min(e, left) * (int)a.dy_stride;
+      for (int u = 0; u < ROWS_Y; ++u) {
+        const uint32_t row = (uint32_t)std::min(t * kStep + PASS_Y * u + my_row, rows - 1);
+        const char* y = base + (uint64_t)row * pitch;
         if constexpr (NARROW) {
-          w[2 * e] = w[2 * e + 1] = 0u;
 #pragma unroll
-          for (int q = 0; q < CY; ++q) {
-            const T v = y[std::min<int64_t>(col + q, width - 1)];
+          for (int i = 0; i < W; ++i) w[W * u + i] = 0u;
+#pragma unroll
+          for (int i = 0; i < kVecY; ++i) {
+            const T v = reinterpret_cast<const T*>(y)[std::min<int64_t>(col + i, width - 1)];
             if constexpr (sizeof(T) == 4)
-              w[2 * e + q] = __builtin_bit_cast(uint32_t, v);
+              w[W * u + i] = __builtin_bit_cast(uint32_t, v);
             else
-              w[2 * e + q / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, v) << (16 * (q & 1));
+              w[W * u + i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, v) << (16 * (i & 1));
           }
         } else {
-          const v2u u = load_at<v2u, sizeof(T)>(reinterpret_cast<const char*>(y) + off);
-          w[2 * e] = u.x;
-          w[2 * e + 1] = u.y;
+#pragma unroll
+          for (int i = 0; i < W; i += 4) {
+            const v4u v = load_at<v4u, sizeof(T)>(y + 4 * i);
+            w[W * u + i] = v.x; w[W * u + i + 1] = v.y; w[W * u + i + 2] = v.z; w[W * u + i + 3] = v.w;
+          }
         }
       }
     }
     __builtin_amdgcn_sched_barrier(0);  // the sets' loads in order: waits count them
   };
 
-  float power[8];
-  // column q of the patch of x: eight rows widened, scaled and paired
+  float power[kRowsX];
+  // eight codes widened and scaled: piece q of the thread's four
   auto stage_x = [&](const uint32_t (&s)[16], int buf, int q) __attribute__((always_inline)) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-      const float x0 = (float)(int8_t)(s[e] >> (8 * q)) * power[e];
-      const float x1 = (float)(int8_t)(s[e + 1] >> (8 * q)) * power[e + 1];
+      const uint32_t four = s[2 * q + e / 4] >> (8 * (e & 3));
+      const float x0 = (float)(int8_t)four * power[q / 2], x1 = (float)(int8_t)(four >> 8) * power[q / 2];
       if constexpr (__is_same(T, _Float16)) {
         w[e / 2] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x0) |
                    ((uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x1) << 16);
@@ -194,82 +225,93 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
         w[e / 2] = upper_pair(__builtin_bit_cast(uint32_t, x0), __builtin_bit_cast(uint32_t, x1));
       }
     }
-    lds_x[buf][chunk_at(c + q, k)] = v4u{w[0], w[1], w[2], w[3]};
+    lds_x[buf][piece_at(my_row + PASS_X * (q / 2), 2 * in_row + (q & 1), kTileX)] = v4u{w[0], w[1], w[2], w[3]};
   };
-  // column q of the patch of dy, fp32 in three parts
+  // eight values of row q of the thread's rows of dy, fp32 in three parts
   auto stage_y = [&](const uint32_t (&s)[16], int buf, int q) __attribute__((always_inline)) {
-    uint32_t w[P][4];
+    const int at = piece_at(my_row + PASS_Y * q, in_row, TY);
+    if constexpr (P == 1) {
+      lds_y[buf][0][at] = v4u{s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]};
+    } else {
+      uint32_t w[P][4];
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-      if constexpr (P == 3) {
+      for (int e = 0; e < 8; e += 2) {
         uint32_t a3[3], b3[3];
-        cut3(__builtin_bit_cast(float, s[2 * e + q]), a3);
-        cut3(__builtin_bit_cast(float, s[2 * e + 2 + q]), b3);
+        cut3(__builtin_bit_cast(float, s[8 * q + e]), a3);
+        cut3(__builtin_bit_cast(float, s[8 * q + e + 1]), b3);
 #pragma unroll
         for (int p = 0; p < 3; ++p) w[p][e / 2] = upper_pair(a3[p], b3[p]);
-      } else {
-        const uint32_t u = s[2 * e + q / 2], v = s[2 * e + 2 + q / 2];
-        w[0][e / 2] = (q & 1) ? upper_pair(u, v) : lower_pair(u, v);
       }
-    }
 #pragma unroll
-    for (int p = 0; p < P; ++p) lds_y[buf][p][chunk_at(c + q, k)] = v4u{w[p][0], w[p][1], w[p][2], w[p][3]};
+      for (int p = 0; p < P; ++p) lds_y[buf][p][at] = v4u{w[p][0], w[p][1], w[p][2], w[p][3]};
+    }
   };
 
-  // a lane's chunk of column 16 m + (lane & 15) is at 64 m + place[m % 4]
-  int place[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) place[j] = chunk_at(lane & 15, lane >> 4) ^ (4 * j);
+  // byte addresses of a lane's part of 16 columns, for its wave's m-th
   const int wx = (wave % WAVES_X) * kWaveX, wy = (wave / WAVES_X) * S::kWaveY;
+  uint32_t at_x[MX], at_y[NY];
+  {
+    const int row = (lane >> 4) * 8 + ((lane & 15) >> 2), part = (lane & 3) * 8;
+#pragma unroll
+    for (int m = 0; m < MX; ++m)
+      at_x[m] = (uint32_t)(row * kTileX * 2 + ((wx / 16 + m) ^ segment_key(row)) * 32 + part);
+#pragma unroll
+    for (int n = 0; n < NY; ++n)
+      at_y[n] = (uint32_t)(row * TY * 2 + ((wy / 16 + n) ^ segment_key(row)) * 32 + part);
+  }
   v4f acc[MX][NY];
 #pragma unroll
   for (int m = 0; m < MX; ++m)
 #pragma unroll
     for (int n = 0; n < NY; ++n) acc[m][n] = v4f{0.f, 0.f, 0.f, 0.f};
   // dbias: the tiles of one column of dy take the steps in turn
-  float sum[CY];
+  float sum[kVecY];
 #pragma unroll
-  for (int q = 0; q < CY; ++q) sum[q] = 0.f;
+  for (int q = 0; q < kVecY; ++q) sum[q] = 0.f;
   int turn = (int)tile_i;  // steps until this tile's next
 
   // step t's loads made ready to be staged
-  auto settle = [&](auto x_wave, uint32_t (&w)[16], int t) __attribute__((always_inline)) {
+  auto settle = [&](auto x_wave, uint32_t (&w)[16], const uint32_t (&b)[kRowsX], int t) __attribute__((always_inline)) {
     if constexpr (decltype(x_wave)::value) {
       if (shifts) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] >>= shift;
+        for (int u = 0; u < kRowsX; ++u) shift_down(&w[4 * u], shift);
       }
-      // this lane's power of two, and those of its own columns in all rows
-      // from the lanes that hold them
-      const float own = w[8] == 255u ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(1.f, (int)w[8] - 127);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        power[e] = __builtin_bit_cast(
-            float, __builtin_amdgcn_ds_bpermute((e * 8 + (lane >> 3)) * 4, __builtin_bit_cast(int, own)));
+      for (int u = 0; u < kRowsX; ++u) power[u] = scale_value(b[u]);
     } else {
       if (shifts) {
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint64_t v = ((uint64_t)w[2 * e + 1] << 32 | w[2 * e]) >> shift;
-          w[2 * e] = (uint32_t)v;
-          w[2 * e + 1] = (uint32_t)(v >> 32);
+          for (int u = 0; u < ROWS_Y; ++u) shift_down(&w[4 * u], shift);
+        } else {
+#pragma unroll
+          for (int u = 0; u < ROWS_Y; ++u)
+#pragma unroll
+            for (int bit = 0; bit < 3; ++bit)
+              if ((shift >> (5 + bit)) & 1) {
+#pragma unroll
+                for (int i = 0; i + (1 << bit) < 8; ++i) w[8 * u + i] = w[8 * u + i + (1 << bit)];
+              }
         }
       }
       if ((t + 1) * kStep > rows) {  // trim: no row past the split's end counts
-        const int left = rows - t * kStep - 8 * k;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e >= left) w[2 * e] = w[2 * e + 1] = 0u;
+        for (int u = 0; u < ROWS_Y; ++u)
+          if (t * kStep + PASS_Y * u + my_row >= rows) {
+#pragma unroll
+            for (int i = 0; i < 16 / ROWS_Y; ++i) w[16 / ROWS_Y * u + i] = 0u;
+          }
       }
       if (turn == 0) {
 #pragma unroll
-        for (int q = 0; q < CY; ++q)
+        for (int u = 0; u < ROWS_Y; ++u)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int q = 0; q < kVecY; ++q) {
             if constexpr (P == 3)
-              sum[q] += __builtin_bit_cast(float, w[2 * e + q]);
+              sum[q] += __builtin_bit_cast(float, w[8 * u + q]);
             else
-              sum[q] += (float)__builtin_bit_cast(T, (uint16_t)(w[2 * e + q / 2] >> (16 * (q & 1))));
+              sum[q] += (float)__builtin_bit_cast(T, (uint16_t)(w[4 * u + q / 2] >> (16 * (q & 1))));
           }
         turn = (int)l.tiles_in;
       }
@@ -283,14 +325,14 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
       stage_y(w, buf, q);
   };
   auto walk = [&](auto x_wave) __attribute__((always_inline)) {
-    constexpr int PIECES = decltype(x_wave)::value ? CX : CY, GROUPS = P * NY;
+    constexpr int PIECES = decltype(x_wave)::value ? 2 * kRowsX : ROWS_Y, GROUPS = P * NY;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) read(x_wave, set[u], u);
-    settle(x_wave, set[0], 0);
+    for (int u = 0; u < kAhead; ++u) read(x_wave, set[u], byte[u], u);
+    settle(x_wave, set[0], byte[0], 0);
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) piece(x_wave, set[0], 0, q);
     __builtin_amdgcn_sched_barrier(0);
-    read(x_wave, set[0], kAhead);
+    read(x_wave, set[0], byte[0], kAhead);
     __syncthreads();
     // whole rounds of sets: a step past the last adds zeros, where a way out
     // inside the round would make every wait for loads one for all of them
@@ -302,20 +344,20 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
         // step's staging into the next buffer, in one basic block, so that
         // the vector unit works while the matrix unit is busy.  (Past the
         // last step the staging writes what nobody reads.)
-        settle(x_wave, set[later], t + 1);
+        settle(x_wave, set[later], byte[later], t + 1);
         v4u fx[MX], fy[2];
 #pragma unroll
-        for (int m = 0; m < MX; ++m) fx[m] = lds_x[u][wx * 4 + 64 * m + place[m % 4]];
-        fy[0] = lds_y[u][0][wy * 4 + place[0]];
+        for (int m = 0; m < MX; ++m) fx[m] = turned(lds_x[u], at_x[m], kTileX * 2);
+        fy[0] = turned(lds_y[u][0], at_y[0], TY * 2);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
           const int n = g % NY, next = g + 1;
-          if (next < GROUPS) fy[next % 2] = lds_y[u][next / NY][wy * 4 + 64 * (next % NY) + place[next % NY % 4]];
+          if (next < GROUPS) fy[next % 2] = turned(lds_y[u][next / NY], at_y[next % NY], TY * 2);
 #pragma unroll
           for (int m = 0; m < MX; ++m) acc[m][n] = multiply<T>(fx[m], fy[g % 2], acc[m][n]);
           if ((g + 1) * PIECES / GROUPS > g * PIECES / GROUPS) piece(x_wave, set[later], later, g * PIECES / GROUPS);
         }
-        read(x_wave, set[later], t + 1 + kAhead);
+        read(x_wave, set[later], byte[later], t + 1 + kAhead);
         __syncthreads();
       }
     }
@@ -343,17 +385,18 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
   }
   if (a.dbias) {
     // the row groups' sums, added in their order
-    float* sums = reinterpret_cast<float*>(&lds_x[0][0]);  // [4][kTileY]; every wave is past its reads
+    float* sums = reinterpret_cast<float*>(&lds_x[0][0]);  // [PASS_Y][TY]; every wave is past its reads
+    static_assert(PASS_Y * TY * sizeof(float) <= sizeof(lds_x), "fits");
     if (!is_x) {
 #pragma unroll
-      for (int q = 0; q < CY; ++q) sums[k * S::kTileY + c + q] = sum[q];
+      for (int q = 0; q < kVecY; ++q) sums[my_row * TY + c + q] = sum[q];
     }
     __syncthreads();
     const int64_t o = o0 + tid;
-    if (tid < S::kTileY && o < a.out) {
+    if (tid < TY && o < a.out) {
       float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < kChunks; ++e) s += sums[e * S::kTileY + tid];
+      for (int e = 0; e < PASS_Y; ++e) s += sums[e * TY + tid];
       reinterpret_cast<float*>(a.ws + l.bias)[(split * l.tiles_in + tile_i) * a.out + o] = s;
     }
   }
@@ -429,7 +472,7 @@ hipError_t launch_linear_grad(int dtype, const LinearGradArgs& a, hipStream_t st
   const unsigned blocks = (unsigned)(l.tiles_out * l.tiles_in * l.splits);
   hipError_t e = with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    if (a.out < Shape<T>::kColsY || a.in < kColsX)
+    if (a.out < kVecY || a.in < kVecX)
       linear_grad_kernel<T, true><<<blocks, kThreads, 0, st>>>(a, l);
     else
       linear_grad_kernel<T, false><<<blocks, kThreads, 0, st>>>(a, l);
