@@ -46,6 +46,7 @@ template <>
 struct Shape<float> {
   static constexpr int kParts = 3, kTileY = 128, kWaveY = 64;
 };
+constexpr int kXCDs = 8, kRunSteps = 128;
 constexpr int kAhead = 2;  // steps whose loads are in flight, and buffers in LDS
 
 template <typename T>
@@ -127,8 +128,15 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
   __shared__ v4u lds_y[kAhead][P][kStep * TY / 8];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
 
+  // Workgroups are dealt to the eight XCDs in turn.  Where splits are long,
+  // each XCD takes a run of consecutive tiles, which share rows of dy and x in
+  // its L2.  65536 x 4096 x 1024 bf16 (512 steps a split): 484 us against 533
+  // without; 2047 x 769 x 1001 fp32 (8 steps): 36 against 32; equal at 64.
+  const uint32_t xcd = blockIdx.x % kXCDs, whole = gridDim.x / kXCDs, rest = gridDim.x % kXCDs;
+  const uint32_t block =
+      l.split_rows >= kRunSteps * kStep ? xcd * whole + std::min(xcd, rest) + blockIdx.x / kXCDs : blockIdx.x;
   const int64_t tiles = l.tiles_out * l.tiles_in;
-  const int64_t split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
+  const int64_t split = block / tiles, tile = block - split * tiles;
   const int64_t tile_o = tile / l.tiles_in, tile_i = tile - tile_o * l.tiles_in;
   const int64_t o0 = tile_o * TY, i0 = tile_i * kTileX;
   const int64_t r_begin = split * l.split_rows;
@@ -345,16 +353,17 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
         // the vector unit works while the matrix unit is busy.  (Past the
         // last step the staging writes what nobody reads.)
         settle(x_wave, set[later], byte[later], t + 1);
-        v4u fx[MX], fy[2];
+        v4u fx[MX], fy[3];  // dy's columns are read two groups ahead
 #pragma unroll
         for (int m = 0; m < MX; ++m) fx[m] = turned(lds_x[u], at_x[m], kTileX * 2);
-        fy[0] = turned(lds_y[u][0], at_y[0], TY * 2);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) fy[g] = turned(lds_y[u][g / NY], at_y[g % NY], TY * 2);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-          const int n = g % NY, next = g + 1;
-          if (next < GROUPS) fy[next % 2] = turned(lds_y[u][next / NY], at_y[next % NY], TY * 2);
+          const int n = g % NY, next = g + 2;
+          if (next < GROUPS) fy[next % 3] = turned(lds_y[u][next / NY], at_y[next % NY], TY * 2);
 #pragma unroll
-          for (int m = 0; m < MX; ++m) acc[m][n] = multiply<T>(fx[m], fy[g % 2], acc[m][n]);
+          for (int m = 0; m < MX; ++m) acc[m][n] = multiply<T>(fx[m], fy[g % 3], acc[m][n]);
           if ((g + 1) * PIECES / GROUPS > g * PIECES / GROUPS) piece(x_wave, set[later], later, g * PIECES / GROUPS);
         }
         read(x_wave, set[later], byte[later], t + 1 + kAhead);

@@ -599,6 +599,20 @@ def test_linear_grad(gpu, rows, out, width, dtype):
         assert torch.equal(again[0], dw) and again[1] is None
 
 
+@pytest.mark.parametrize("rows,out,width,dtype", [(4100, 3800, 4200, BF16), (9000, 1700, 4500, F16),
+                                                  (9000, 850, 4500, F32)])
+def test_linear_grad_long_splits(gpu, rows, out, width, dtype):
+    """Enough tiles that a workgroup walks over 4096 rows, one or two splits,
+    workgroups that do not divide by eight."""
+    flush_print(f"linear_grad rows={rows} out={out} in={width} {dtype}")
+    dy, codes, scales, x = linear_case(75, rows, out, width, dtype)
+    bw, bb = linear_bound(dy, x, rows, dtype)
+    dw, db = A.linear_grad(dy, codes, scales, dtype=F32)
+    rw, rb = dy.double().t() @ x, dy.double().sum(0)
+    within(dw, rw, bw + 2 * E * rw.abs() + TINY[F32], "dweight")
+    within(db, rb, bb + 2 * E * rb.abs() + TINY[F32], "dbias")
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 @pytest.mark.parametrize("rows", [100, 3000])
 def test_linear_grad_into_segments(gpu, rows, dtype):
