@@ -248,7 +248,7 @@ def _norm(x, weight, bias, eps, out, stream, keep):
             codes = _fresh(x, torch.int8)
             scales = torch.empty((*lead, _blocks(hidden)), dtype=torch.uint8, device=dev)
         else:
-            mean = torch.empty(lead, dtype=torch.float32, device=dev)
+            mean = torch.empty_like(rstd)
         _native.check(_native.lib().adasum_layer_norm(
             x.data_ptr(), rows, hidden, stride, code, _ptr(weight), _ptr(bias), param_code, eps, y.data_ptr(),
             out_stride, _ptr(mean), rstd.data_ptr(), _ptr(codes), _ptr(scales), st))
