@@ -189,12 +189,16 @@ __device__ __forceinline__ float lane_value(float x, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
 
-// The sum over the wave's 64 lanes, in a fixed order, the same in every lane.
-__device__ __forceinline__ float wave_sum(float x) {
+// The sum over 16 neighbouring lanes or over the wave's 64, in a fixed order,
+// the same in every lane.
+__device__ __forceinline__ float sum16(float x) {
   x += dpp<kXor1>(x);
   x += dpp<kXor2>(x);
   x += dpp<kHalfMirror>(x);
-  x += dpp<kMirror>(x);
+  return x + dpp<kMirror>(x);
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  x = sum16(x);
   return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
 }
 

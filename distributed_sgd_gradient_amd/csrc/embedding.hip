@@ -180,7 +180,7 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a) {
       // Where many rows are owned, most of them have one frequent token: the
       // first one's rows are counted with one addition, where LDS would make
       // them one by one.  131072 rows of one token: 183 us for this kernel
-      // without, 67 with; 45 rows a step of two tokens: 76 us and 84 with it
+      // without, 67 with; about 45 rows a step: 76 us, and 88 if counted so
       // from eight rows on, hence the bound.
       const int owned = __popcll(met[0]) + __popcll(met[1]) + __popcll(met[2]) + __popcll(met[3]);
       if (owned > kCrowd) {

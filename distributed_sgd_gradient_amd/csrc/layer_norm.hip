@@ -7,9 +7,16 @@
 //              dx = r (g - mean(g) - n mean(g n)),
 //              dw = sum over rows of dy n, db = sum over rows of dy
 //
-// A row is held in registers by `LPR` lanes, NV vectors of 16 bytes each, so
-// it is read once.  LPR is one wave for rows of up to 16 values per lane
-// (no LDS, no barrier), else a workgroup of 256 or 1024 lanes.
+// Bound by HBM: a row is held in registers by `LPR` lanes, NV vectors of 16
+// bytes each, so it is read once, and the next row's loads are on their way
+// while one is worked on.  LPR is 16 lanes or one wave for rows of up to 16
+// values per lane (no LDS, no barrier), else a workgroup of 256 or 1024 lanes.
+// 524288 x 128 bf16, forward: 54 us with 16 lanes a row, 152 with 64.
+//
+// Measured, bf16 (fp32 parameters): forward of 65536 x 1024 with kept rows 79
+// us (4.3 TB/s), 524288 x 128 54 us (5.0), 8192 x 16384 115 us (4.7); backward
+// of 65536 x 1024 from x 75 + 5 us (5.1), 524288 x 128 81 us (5.0), 8192 x
+// 16384 162 us (5.0).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -28,7 +35,7 @@ using namespace elem;
 template <int LPR, int N>
 __device__ __forceinline__ void row_sum(float (&s)[N], float (*lds)[N][LPR / 64 > 0 ? LPR / 64 : 1], int slot) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = wave_sum(s[i]);
+  for (int i = 0; i < N; ++i) s[i] = LPR == 16 ? sum16(s[i]) : wave_sum(s[i]);
   if constexpr (LPR > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -152,13 +159,28 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_grad_kernel(NormGr
   int valid[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) valid[j] = H - (j * LPR + lane) * VEC;
-  float w[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+  // 1024 lanes have 128 registers each: there the weights, and for fp32 the
+  // sums of dy, lie in LDS, every lane its own (8192 x 16384 bf16: 164 us
+  // against 230 with spilled registers; 4096 x 16384 fp32: 177, with only the
+  // weights 241, with neither 310)
+  constexpr bool LDS_W = LPR == 1024, LDS_B = LDS_W && sizeof(T) == 4;
+  __shared__ float far[LDS_W ? NV * LPR * VEC : 1], far_b[LDS_B ? NV * LPR * VEC : 1];
+  float w[LDS_W ? 1 : NV][VEC], aw[NV][VEC], ab[LDS_B ? 1 : NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      w[j][i] = i < valid[j] ? (a.weight ? load_any(a.weight, a.param_dtype, (j * LPR + lane) * VEC + i) : 1.f) : 0.f;
-      aw[j][i] = ab[j][i] = 0.f;
+      const int c = (j * LPR + lane) * VEC + i;
+      const float v = i < valid[j] ? (a.weight ? load_any(a.weight, a.param_dtype, c) : 1.f) : 0.f;
+      if constexpr (LDS_W)
+        far[c] = v;
+      else
+        w[j][i] = v;
+      aw[j][i] = 0.f;
+      if constexpr (LDS_B)
+        far_b[c] = 0.f;
+      else
+        ab[j][i] = 0.f;
     }
   const T* dy = static_cast<const T*>(a.dy);
   const T* x = static_cast<const T*>(a.x);
@@ -212,8 +234,11 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_grad_kernel(NormGr
       for (int i = 0; i < VEC; ++i) {
         const float d = g[j][i];
         aw[j][i] = __builtin_fmaf(d, n[j][i], aw[j][i]);
-        ab[j][i] += d;
-        g[j][i] = d * w[j][i];
+        if constexpr (LDS_B)
+          far_b[(j * LPR + lane) * VEC + i] += d;
+        else
+          ab[j][i] += d;
+        g[j][i] = d * (LDS_W ? far[LDS_W ? (j * LPR + lane) * VEC + i : 0] : w[LDS_W ? 0 : j][i]);
         s[0] += g[j][i];
         s[1] = __builtin_fmaf(g[j][i], n[j][i], s[1]);
       }
@@ -231,37 +256,54 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void norm_grad_kernel(NormGr
   // The workgroup's sums: its waves' rows added in wave order through LDS,
   // one wave's columns at a time.
   float* out = a.partials + (int64_t)blockIdx.x * 2 * H;
-  if constexpr (LPR == 64) {
-    __shared__ float part[3][2][64 * VEC];
+  if constexpr (LPR <= 64) {
+    __shared__ float part[3][2][LPR * VEC];
     const int wave = threadIdx.x >> 6;
+    if constexpr (LPR == 16) {  // the wave's four rows first
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+          for (int d = 16; d < 64; d *= 2) {
+            aw[j][i] += __shfl_xor(aw[j][i], d);
+            ab[j][i] += __shfl_xor(ab[j][i], d);
+          }
+    }
+    const bool first = (threadIdx.x & 63) < LPR;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (j > 0) __syncthreads();
-      if (wave > 0) {
+      if (wave > 0 && first) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          part[wave - 1][0][i * 64 + lane] = aw[j][i];
-          part[wave - 1][1][i * 64 + lane] = ab[j][i];
+          part[wave - 1][0][i * LPR + lane] = aw[j][i];
+          part[wave - 1][1][i * LPR + lane] = ab[j][i];
         }
       }
       __syncthreads();
-      if (wave == 0) {
+      if (wave == 0 && first) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
 #pragma unroll
           for (int q = 0; q < 3; ++q) {
-            aw[j][i] += part[q][0][i * 64 + lane];
-            ab[j][i] += part[q][1][i * 64 + lane];
+            aw[j][i] += part[q][0][i * LPR + lane];
+            ab[j][i] += part[q][1][i * LPR + lane];
           }
-        store_row<float, VEC>(out + (j * 64 + lane) * VEC, aw[j], valid[j]);
-        store_row<float, VEC>(out + H + (j * 64 + lane) * VEC, ab[j], valid[j]);
+        store_row<float, VEC>(out + (j * LPR + lane) * VEC, aw[j], valid[j]);
+        store_row<float, VEC>(out + H + (j * LPR + lane) * VEC, ab[j], valid[j]);
       }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      store_row<float, VEC>(out + (j * LPR + lane) * VEC, aw[j], valid[j]);
-      store_row<float, VEC>(out + H + (j * LPR + lane) * VEC, ab[j], valid[j]);
+      const int c = (j * LPR + lane) * VEC;
+      if constexpr (LDS_B) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ab[0][i] = far_b[c + i];
+      }
+      store_row<float, VEC>(out + c, aw[j], valid[j]);
+      store_row<float, VEC>(out + H + c, ab[LDS_B ? 0 : j], valid[j]);
     }
   }
 }
@@ -314,6 +356,7 @@ struct GradShape {
 };
 GradShape grad_shape(int hidden) {
   const int per_wave = 64 * 16;
+  if (hidden <= 16 * 16) return {16, 256, 16};
   if (hidden <= per_wave) return {64, 256, 4};
   if (hidden <= 4 * per_wave) return {256, 256, 1};
   return {1024, 1024, 1};
@@ -334,6 +377,8 @@ hipError_t norm_grad_width(const NormGradArgs& a, int lanes, int blocks, hipStre
   constexpr int NV = 16 / Type<T>::kVec;
   const int64_t nvec = ceil_div(a.hidden, Type<T>::kVec);
   const bool half = nvec <= (int64_t)lanes * NV / 2;
+  if (lanes == 16)
+    return half ? norm_grad_launch<T, 16, NV / 2>(a, blocks, st) : norm_grad_launch<T, 16, NV>(a, blocks, st);
   if (lanes == 64)
     return half ? norm_grad_launch<T, 64, NV / 2>(a, blocks, st) : norm_grad_launch<T, 64, NV>(a, blocks, st);
   if (lanes == 256)
@@ -346,6 +391,8 @@ hipError_t norm_width(const NormArgs& a, hipStream_t st) {
   constexpr int VEC = Type<T>::kVec;
   constexpr int NV = 16 / VEC;
   const int64_t nvec = ceil_div(a.hidden, VEC);
+  if (nvec <= 16 * NV / 2) return norm_launch<T, 16, NV / 2>(a, st);
+  if (nvec <= 16 * NV) return norm_launch<T, 16, NV>(a, st);
   if (nvec <= 64 * NV / 2) return norm_launch<T, 64, NV / 2>(a, st);
   if (nvec <= 64 * NV) return norm_launch<T, 64, NV>(a, st);
   if (nvec <= 256 * NV / 2) return norm_launch<T, 256, NV / 2>(a, st);
@@ -362,11 +409,12 @@ hipError_t launch_norm(int dtype, const NormArgs& a, hipStream_t st) {
 
 int norm_grad_blocks(int64_t rows, int hidden) {
   const GradShape s = grad_shape(hidden);
-  // Two workgroups of 256 lanes per CU, or as many waves in wider ones, and
-  // no more than leaves each four rows a wave: every workgroup leaves a row of
-  // partial sums for the join.  65536 x 1024 bf16: 75 us whether 512 or 1024
-  // workgroups, the join 5 against 8 us.
-  return (int)std::min<int64_t>(ceil_div(rows, s.rows * 4), (int64_t)kCUs * 512 / s.threads);
+  // Two workgroups of 256 lanes per CU, or as many waves in wider ones, but
+  // one per CU at least; and no more than leaves a wave four rows, or 16 lanes
+  // two: every workgroup leaves a row of partial sums for the join.  65536 x
+  // 1024 bf16: 75 us whether 512 or 1024 workgroups, the join 5 against 8 us.
+  return (int)std::min<int64_t>(ceil_div(rows, s.rows * (s.lanes == 16 ? 2 : 4)),
+                                std::max<int64_t>(kCUs, (int64_t)kCUs * 512 / s.threads));
 }
 
 hipError_t launch_norm_grad(int dtype, const NormGradArgs& a, hipStream_t st) {

@@ -376,8 +376,10 @@ def plain_norm_grad(dy, n, rstd, weight):
 
 
 def chain(rows, hidden):
-    """Rows that one wave or workgroup of the backward pass adds up (at least
-    four, so that few partial sums are left), and the three other waves."""
+    """Rows that one wave or workgroup of the backward pass adds up at most (at
+    least four, so that few partial sums are left), and the three other waves.
+    Up to 256 wide, 16 lanes add up a quarter as many or two, and two steps
+    across the wave follow: no more than that."""
     groups = 512 * 4 if hidden <= 1024 else 512 if hidden <= 4096 else 128
     return max(4, -(-rows // groups)) + 3
 
@@ -404,6 +406,27 @@ def test_layer_norm_grad(gpu, hidden, dtype, kept):
         c = chain(rows, hidden)
         within(dw, rw, (c + 4) * E * mw + E * rw.abs(), "dweight")
         within(db, rb, c * E * mb + E * rb.abs(), "dbias")
+
+
+@pytest.mark.parametrize("rows,hidden,dtype", [(20001, 40, BF16), (20003, 128, F32), (9001, 250, F16),
+                                               (6001, 700, BF16), (1500, 4000, F16), (700, 9000, F32),
+                                               (1030, 16384, BF16), (600, 16383, F32)])
+def test_layer_norm_grad_many_rows(gpu, rows, hidden, dtype):
+    """Several rows for every group of lanes, at each width that is treated
+    in its own way."""
+    x, dy = randn(36, rows, hidden, dtype=dtype, mean=0.3), randn(37, rows, hidden, dtype=dtype)
+    w = randn(38, hidden, mean=1.0, std=0.3)
+    flush_print(f"layer_norm_grad rows={rows} hidden={hidden} {dtype}")
+    y, mean, rstd = A.layer_norm(x, w)
+    ry, _, _, n = plain_norm(x, w, None, 1e-5)
+    within(y, ry, norm_bounds(ry, n, w, None, dtype)[0], "y")
+    n = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    rx, rw, rb, mx, mw, mb = plain_norm_grad(dy, n, rstd, w)
+    dx, dw, db = A.layer_norm_grad(dy, x, mean, rstd, w)
+    within(dx, rx, mx + (U[dtype] + E) * rx.abs() + TINY[dtype], "dx")
+    c = chain(rows, hidden)
+    within(dw, rw, (c + 4) * E * mw + E * rw.abs(), "dweight")
+    within(db, rb, c * E * mb + E * rb.abs(), "dbias")
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
