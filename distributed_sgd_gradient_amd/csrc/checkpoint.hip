@@ -5,7 +5,9 @@
 // Both kernels move each byte once and are bound by HBM.  A lane's piece is
 // 16 bytes of the wider side; the pieces of a row are padded to whole blocks,
 // so that a block's lanes are always neighbours, and pieces are dealt to the
-// lanes across row ends, so that narrow rows fill the waves too.
+// lanes across row ends, so that narrow rows fill the waves too.  16384 x 4096
+// bf16, mostly resident in the memory-side cache: packing 41 us, reading back
+// 31 (5.0 and 6.6 TB/s; a copy of 2 GB reaches 4.8, one of 128 MB 8.6).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -17,6 +17,14 @@
 //           are left for
 //   join    adds them in the order of the list, in fp64.
 // Every sum has a fixed order, so the result is bitwise reproducible.
+//
+// Measured.  Lookup of 65536 rows of 1024 in bf16: 39 us, bound by the writes
+// (134 MB, and 62 MB of table rows).  Gradient of the same 65536 rows, a
+// tenth without token, into 30522 x 1024 fp32: group 27 us, sum 48 (3.8 TB/s of
+// rows in no order), join 6; two tables' worth of bytes, 246 MB, would take 51
+// at the rate of a large copy.  Grouping is bound by its scan, which every
+// workgroup makes of all tokens, and by the workgroup of the most frequent
+// token.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -653,7 +661,8 @@ EmbeddingGradLayout embedding_grad_layout(int64_t n, int hidden, int dtype) {
   l.units = kSumThreads / l.lanes;
   l.tiles = (int)ceil_div(hidden, (int64_t)l.lanes * vec);
   // long spans leave less to join, short ones fill the GPU: the longest of 8
-  // to 32 positions with two workgroups per CU
+  // to 32 positions with two workgroups per CU (65536 rows of 1024: 48 us with
+  // 32; asking for four or eight per CU changed nothing beyond noise)
   l.span = 32;
   while (l.span > 8 && ceil_div(n, (int64_t)l.units * l.span) * l.tiles < 2 * kCUs) l.span /= 2;
   while (l.span > 1 && l.units * l.span > kSumSpots) l.span /= 2;

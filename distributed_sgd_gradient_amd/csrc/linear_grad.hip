@@ -15,6 +15,16 @@
 // So 16-bit dy meets x in its own type; fp32 dy is cut into three bf16 parts
 // of 8 bits each, hi + mid + lo = dy exactly, that meet x one after another.
 // Sums are fp32 within a split of the rows; splits are joined in fp64.
+//
+// Bound by the matrix cores and what shares a CU with them: of 65536 x 4096 x
+// 1024 in bf16, 487 us in all (1129 TFLOP/s; a large library product reaches
+// 1225 on the same card), the matrix instructions and LDS reads alone take 330
+// us, with the loads 340, with the staging (widening the codes, LDS writes)
+// 430.  fp32 dy costs three times the matrix instructions: 16384 x 4096 x 1024
+// in 370 us.  Tried and dropped: a patch of columns turned in registers before
+// LDS (707 us against 590 of the transposing reads, under a profiler), 64 rows
+// a step, three steps of loads ahead (registers spill), raised wave priority
+// around the matrix instructions.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -115,7 +125,7 @@ __device__ __forceinline__ void shift_down(uint32_t* w, int bits) {
 // a wave computes on one LDS buffer while it stages step t + 1 into the next
 // and then asks for step t + 1 + kAhead: one barrier a step, and kAhead steps
 // of loads on their way.
-template <typename T, bool NARROW>
+template <typename T, bool NARROW_X, bool NARROW_Y>
 __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs a, LinearGradLayout l) {
   using S = Shape<T>;
   constexpr int P = S::kParts, TY = S::kTileY;
@@ -149,13 +159,13 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
   // columns across the edge are loaded as the last whole vector of the row
   // and moved down by `shift` bits.  (A matrix narrower than a vector is
   // loaded value by value.)
-  const bool is_x = wave < 4;
+  const bool is_x = wave < 4, narrow = is_x ? NARROW_X : NARROW_Y;
   const int in_row = lane & ((is_x ? LANES_X : LANES_Y) - 1);
   const int my_row = ((wave & 3) * 64 + lane) / (is_x ? LANES_X : LANES_Y);
   const int cols = is_x ? kVecX : kVecY, c = in_row * cols;
   const int64_t width = is_x ? a.in : a.out, col = (is_x ? i0 : o0) + c;
   const int64_t from = col + cols <= width ? col : width - cols;
-  const int shift = !NARROW && col < width && col > from ? (int)(col - from) * (is_x ? 8 : 8 * (int)sizeof(T)) : 0;
+  const int shift = !narrow && col < width && col > from ? (int)(col - from) * (is_x ? 8 : 8 * (int)sizeof(T)) : 0;
   const bool shifts = __ballot(shift != 0) != 0;
 
   // x: two rows of 16 codes, and their scale bytes in `byte`; dy: 64 bytes of
@@ -166,9 +176,9 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
   // split's end read its last row; trim clears dy's), so that the waits for a
   // step's loads leave the later steps' on their way.  A row's offset is 32 x
   // 32 bits.
-  const char* const base = is_x ? reinterpret_cast<const char*>(a.codes + r_begin * a.in + (NARROW ? 0 : from))
+  const char* const base = is_x ? reinterpret_cast<const char*>(a.codes + r_begin * a.in + (narrow ? 0 : from))
                                 : reinterpret_cast<const char*>(static_cast<const T*>(a.dy) + r_begin * a.dy_stride +
-                                                                (NARROW ? 0 : from));
+                                                                (narrow ? 0 : from));
   const uint8_t* const scale_base = a.scales + r_begin * nb + std::min<int64_t>(col / kScaleBlock, nb - 1);
   const uint32_t pitch = is_x ? (uint32_t)a.in : (uint32_t)(a.dy_stride * sizeof(T));
   auto read = [&](auto x_wave, uint32_t (&w)[16], uint32_t (&b)[kRowsX], int t) __attribute__((always_inline)) {
@@ -177,7 +187,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
       for (int u = 0; u < kRowsX; ++u) {
         const uint32_t row = (uint32_t)std::min(t * kStep + PASS_X * u + my_row, rows - 1);
         const char* x = base + (uint64_t)row * pitch;
-        if constexpr (NARROW) {
+        if constexpr (NARROW_X) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[4 * u + i] = 0u;
 #pragma unroll
@@ -195,7 +205,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
       for (int u = 0; u < ROWS_Y; ++u) {
         const uint32_t row = (uint32_t)std::min(t * kStep + PASS_Y * u + my_row, rows - 1);
         const char* y = base + (uint64_t)row * pitch;
-        if constexpr (NARROW) {
+        if constexpr (NARROW_Y) {
 #pragma unroll
           for (int i = 0; i < W; ++i) w[W * u + i] = 0u;
 #pragma unroll
@@ -481,10 +491,17 @@ hipError_t launch_linear_grad(int dtype, const LinearGradArgs& a, hipStream_t st
   const unsigned blocks = (unsigned)(l.tiles_out * l.tiles_in * l.splits);
   hipError_t e = with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    if (a.out < kVecY || a.in < kVecX)
-      linear_grad_kernel<T, true><<<blocks, kThreads, 0, st>>>(a, l);
+    // 65536 rows, bf16: 2 x 1024 outputs 87 us, 1024 x 2 61 us; with both
+    // operands loaded value by value 136 and 141
+    const bool narrow_x = a.in < kVecX, narrow_y = a.out < kVecY;
+    if (narrow_x && narrow_y)
+      linear_grad_kernel<T, true, true><<<blocks, kThreads, 0, st>>>(a, l);
+    else if (narrow_x)
+      linear_grad_kernel<T, true, false><<<blocks, kThreads, 0, st>>>(a, l);
+    else if (narrow_y)
+      linear_grad_kernel<T, false, true><<<blocks, kThreads, 0, st>>>(a, l);
     else
-      linear_grad_kernel<T, false><<<blocks, kThreads, 0, st>>>(a, l);
+      linear_grad_kernel<T, false, false><<<blocks, kThreads, 0, st>>>(a, l);
     return hipGetLastError();
   });
   if (e != hipSuccess || (l.direct && !a.dbias)) return e;

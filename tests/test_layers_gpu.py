@@ -608,7 +608,8 @@ def linear_bound(dy, x, rows, dtype):
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 @pytest.mark.parametrize("rows,out,width", [(1, 1, 1), (1, 130, 70), (2, 5, 33), (31, 128, 128), (33, 129, 127),
                                             (64, 64, 256), (65, 3, 1001), (500, 200, 300), (1025, 131, 37),
-                                            (4096, 256, 128), (9999, 17, 65)])
+                                            (4096, 256, 128), (9999, 17, 65), (3000, 200, 9), (3000, 5, 200),
+                                            (3000, 7, 15), (3000, 8, 16)])
 def test_linear_grad(gpu, rows, out, width, dtype):
     flush_print(f"linear_grad rows={rows} out={out} in={width} {dtype}")
     dy, codes, scales, x = linear_case(70, rows, out, width, dtype)
