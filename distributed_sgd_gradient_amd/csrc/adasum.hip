@@ -321,7 +321,7 @@ int validate_buffers(const void* const* grads, int K, int64_t N, size_t esz, int
 // pointer, or a buffer on another GPU, would otherwise fault inside a
 // kernel).  Failed queries are cleared so that they cannot surface later as
 // the error of a launch.
-int check_device_range(const void* p, size_t bytes, const char* name, int device) {
+int check_device_range(const void* p, size_t bytes, const char* name, int device, uintptr_t* from, uintptr_t* to) {
   char buf[200];
   hipPointerAttribute_t attr;
   if (hipPointerGetAttributes(&attr, p) != hipSuccess) {
@@ -348,6 +348,10 @@ int check_device_range(const void* p, size_t bytes, const char* name, int device
   if (a < lo || a + bytes > end) {
     snprintf(buf, sizeof buf, "%s: %zu bytes from this address run past the end of its allocation", name, bytes);
     return fail(ADASUM_EINVAL, buf);
+  }
+  if (from && attr.type == hipMemoryTypeDevice) {
+    *from = lo;
+    *to = end;
   }
   return ADASUM_OK;
 }

@@ -71,8 +71,10 @@ int check_devices(const void* const* grads, int K, size_t vec_bytes, const void*
                   int nseg, int device);
 
 // p is device memory of `device`, with `bytes` bytes from it inside its
-// allocation where the runtime knows that allocation's extent.
-int check_device_range(const void* p, size_t bytes, const char* name, int device);
+// allocation where the runtime knows that allocation's extent (which *lo and
+// *end are then set to, where asked for).
+int check_device_range(const void* p, size_t bytes, const char* name, int device, uintptr_t* lo = nullptr,
+                       uintptr_t* end = nullptr);
 
 // ADASUM_LOG is set: launches are traced on stderr.
 bool log_enabled();

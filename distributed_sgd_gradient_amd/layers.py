@@ -128,6 +128,11 @@ def _workspace(workspace, need, dev):
     return workspace
 
 
+def _lead(t, rows):
+    """t's shape without the last dimension (slicing a torch.Size is slow)."""
+    return (rows,) if t.dim() == 2 else t.shape[:-1]
+
+
 def _fresh(t, dtype):
     """A dense tensor of t's shape; empty_like is the cheapest way to one."""
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
@@ -241,7 +246,7 @@ def _norm(x, weight, bias, eps, out, stream, keep):
 
     def body(st):
         y = _fresh(x, x.dtype) if out is None else out
-        lead = x.shape[:-1]
+        lead = _lead(x, rows)
         rstd = torch.empty(lead, dtype=torch.float32, device=dev)
         mean = codes = scales = None
         if keep:
@@ -357,7 +362,7 @@ def checkpoint_pack(x, *, codes=None, scales=None, stream=None):
     dev = _on(x, "x").device
     rows, width, stride = _rows(x, "x")
     code = _code(x.dtype, "x")
-    shape = (*x.shape[:-1], _blocks(width))
+    shape = (*_lead(x, rows), _blocks(width))
     if codes is not None:
         _dense(codes, "codes", dev, x.shape, torch.int8)
     if scales is not None:
