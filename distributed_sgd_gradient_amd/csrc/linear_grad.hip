@@ -17,8 +17,8 @@
 // Sums are fp32 within a split of the rows; splits are joined in fp64.
 //
 // Bound by the matrix cores and what shares a CU with them: of 65536 x 4096 x
-// 1024 in bf16, 487 us in all (1129 TFLOP/s; a large library product reaches
-// 1225 on the same card), the matrix instructions and LDS reads alone take 330
+// 1024 in bf16, 485 to 508 us in all on different cards (1080 to 1130 TFLOP/s;
+// a large library product reaches 1225), the matrix instructions and LDS reads alone take 330
 // us, with the loads 340, with the staging (widening the codes, LDS writes)
 // 430.  fp32 dy costs three times the matrix instructions: 16384 x 4096 x 1024
 // in 370 us.  Tried and dropped: a patch of columns turned in registers before
@@ -229,12 +229,16 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
   };
 
   float power[kRowsX];
-  // eight codes widened and scaled: piece q of the thread's four
+  // Eight codes widened and scaled: piece q of the thread's four.  Every other
+  // four lanes take a row's second half first, so that eight lanes' pieces
+  // fill 128 bytes of banks (without: eight more cycles a write; 65536 x 4096
+  // x 1024 in turns 516 us against 508).
+  const int second = (lane >> 2) & 1;
   auto stage_x = [&](const uint32_t (&s)[16], int buf, int q) __attribute__((always_inline)) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-      const uint32_t four = s[2 * q + e / 4] >> (8 * (e & 3));
+      const uint32_t four = (second ? s[(2 * q + e / 4) ^ 2] : s[2 * q + e / 4]) >> (8 * (e & 3));
       const float x0 = (float)(int8_t)four * power[q / 2], x1 = (float)(int8_t)(four >> 8) * power[q / 2];
       if constexpr (__is_same(T, _Float16)) {
         w[e / 2] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x0) |
@@ -243,7 +247,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
         w[e / 2] = upper_pair(__builtin_bit_cast(uint32_t, x0), __builtin_bit_cast(uint32_t, x1));
       }
     }
-    lds_x[buf][piece_at(my_row + PASS_X * (q / 2), 2 * in_row + (q & 1), kTileX)] = v4u{w[0], w[1], w[2], w[3]};
+    lds_x[buf][piece_at(my_row + PASS_X * (q / 2), 2 * in_row + ((q & 1) ^ second), kTileX)] = v4u{w[0], w[1], w[2], w[3]};
   };
   // eight values of row q of the thread's rows of dy, fp32 in three parts
   auto stage_y = [&](const uint32_t (&s)[16], int buf, int q) __attribute__((always_inline)) {
