@@ -68,8 +68,8 @@ __device__ __forceinline__ v4f multiply(v4u a, v4u b, v4f c) {
 }
 
 // hi + mid + lo = v, each a bf16 (as the upper half of an fp32): cutting off
-// the low bits leaves remainders that are exact.  An infinity or NaN stays in
-// hi.
+// the low bits leaves remainders that are exact.  Bits of v below 2^-133, the
+// least bf16, are lost.  An infinity or NaN stays in hi.
 __device__ __forceinline__ void cut3(float v, uint32_t (&part)[3]) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   const bool finite = (u & 0x7f800000u) != 0x7f800000u;
@@ -247,7 +247,8 @@ __global__ __launch_bounds__(kThreads, 2) void linear_grad_kernel(LinearGradArgs
         w[e / 2] = upper_pair(__builtin_bit_cast(uint32_t, x0), __builtin_bit_cast(uint32_t, x1));
       }
     }
-    lds_x[buf][piece_at(my_row + PASS_X * (q / 2), 2 * in_row + ((q & 1) ^ second), kTileX)] = v4u{w[0], w[1], w[2], w[3]};
+    const int at = piece_at(my_row + PASS_X * (q / 2), 2 * in_row + ((q & 1) ^ second), kTileX);
+    lds_x[buf][at] = v4u{w[0], w[1], w[2], w[3]};
   };
   // eight values of row q of the thread's rows of dy, fp32 in three parts
   auto stage_y = [&](const uint32_t (&s)[16], int buf, int q) __attribute__((always_inline)) {
@@ -472,7 +473,8 @@ LinearGradLayout linear_grad_layout(int64_t rows, int64_t out, int64_t in, int d
   // steps, and every split's partial sums as a step of all tiles' outputs.
   int64_t best = 1, cost = INT64_MAX;
   for (int64_t s = 1; s <= std::min<int64_t>(steps, 256) && (s - 1) * tiles < 2 * kCUs; ++s) {
-    const int64_t c = ceil_div(tiles * s, kCUs) * (ceil_div(steps, s) + 4) + (s > 1 ? 2 + ceil_div(s * tiles, kCUs) : 0);
+    const int64_t c =
+        ceil_div(tiles * s, kCUs) * (ceil_div(steps, s) + 4) + (s > 1 ? 2 + ceil_div(s * tiles, kCUs) : 0);
     if (c < cost) {
       cost = c;
       best = s;

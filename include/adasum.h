@@ -334,8 +334,9 @@ ADASUM_API int adasum_checkpoint_unpack(const int8_t* codes, const uint8_t* scal
 /*
  * adasum_linear_grad - the gradient of y = x weight^T + bias from activations
  * kept in 8 bits: dweight[o][i] = sum over rows of dy[r][o] * x[r][i],
- * dbias[o] = sum over rows of dy[r][o].  Products are exact.  in_features and
- * out_features are at most 2^24.
+ * dbias[o] = sum over rows of dy[r][o].  Products are exact (for dweight, bits
+ * of an fp32 dy below 2^-133 do not count).  in_features and out_features are
+ * at most 2^24.
  *
  *   dy           rows x out_features elements of dtype; dy_stride <= 2^28
  *                (of two rows or more).

@@ -674,6 +674,26 @@ def test_linear_grad_exact_cases(gpu):
         assert torch.equal(dw.double().cpu(), want) and torch.equal(db.double().cpu(), di.sum(0))
 
 
+def test_linear_grad_smallest_values(gpu):
+    """Subnormal dy of each type, times powers of two: exact; of fp32 the bits
+    from 2^-133 on.  Sums of 40 equal values are fp32 values but for the last:
+    40 (1 + 2^-23) = 8 (5 + 5 * 2^-23) takes 26 bits, so its sums round, by
+    what linear_bound allows."""
+    for dtype, low, up in ((BF16, [2.0 ** -133, 3 * 2.0 ** -130], 20), (F16, [2.0 ** -24, 5 * 2.0 ** -22], 3),
+                           (F32, [2.0 ** -133, 2.0 ** -120 * (1 + 2.0 ** -13), 2.0 ** -110 * (1 + 2.0 ** -23)], 30)):
+        dy = torch.tensor(low, dtype=torch.float64).to(dtype).cuda().repeat(40, 5)
+        codes, scales = A.checkpoint_pack(torch.full((40, 33), 2.0 ** up, dtype=dtype, device="cuda"))
+        dw, db = A.linear_grad(dy, codes, scales, dtype=F32)
+        want = dy.double().sum(0)
+        rw = (want * 2.0 ** up)[:, None].expand(-1, 33)
+        exact = torch.tensor([v != 2.0 ** -110 * (1 + 2.0 ** -23) for v in low], device="cuda").repeat(5)
+        assert torch.equal(dw.double()[exact], rw[exact]), dtype
+        assert torch.equal(db.double()[exact], want[exact])
+        bw, bb = linear_bound(dy, A.checkpoint_unpack(codes, scales).double(), 40, dtype)
+        within(dw, rw, bw, "dweight")
+        within(db, want, bb, "dbias")
+
+
 def test_linear_grad_infinities_and_nan(gpu):
     """An infinity or NaN of dy stays in its output row, a block without finite
     values in its columns."""
