@@ -988,6 +988,72 @@ def test_sizes_at_the_limits(gpu):
         A.linear_grad(big.as_strided((8, 70), ((1 << 28) + 1, 1)), *A.checkpoint_pack(randn(168, 8, 300, dtype=BF16)))
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(gpu, seed):
+    """Every operator at shapes, types, strides and offsets drawn from a seed."""
+    rng = np.random.default_rng(seed)
+
+    def size(hi):
+        return int(min(hi, 2 ** rng.uniform(0, math.log2(hi + 1))))
+
+    def put(t):
+        return [lambda v: v, strided, lambda v: unaligned(v, int(rng.integers(1, 8)))][rng.integers(0, 3)](t)
+
+    for turn in range(5):
+        dtype, grad = DTYPES[rng.integers(0, 3)], DTYPES[rng.integers(0, 3)]
+        rows, hidden, out, vocab = size(6000), size(5000), size(700), size(40000)
+        rows = min(rows, 2000000 // hidden)
+        vocab = min(vocab, 8000000 // hidden)
+        base = 1000 * seed + 10 * turn
+        flush_print(f"seed={seed} rows={rows} hidden={hidden} out={out} vocab={vocab} {dtype} {grad}")
+        kind = ["uniform", "frequent", "one", "outside"][rng.integers(0, 4)]
+        tok = tokens_of(base, rows, vocab, kind)
+        tok = tok if rng.random() < 0.5 else tok.to(torch.int32)
+
+        table = randn(base + 1, vocab, hidden, dtype=dtype)
+        want = plain_embedding(table, tok, 0.75)
+        x = A.embedding(put(table), tok, scale=0.75, dtype=dtype)
+        within(x, want, want.abs() * (E + U[dtype]) * 1.0001 + TINY[dtype], "embedding")
+
+        dy = randn(base + 2, rows, hidden, dtype=dtype)
+        ref, mag = plain_embedding_grad(dy, tok, vocab, 0.75)
+        got = A.embedding_grad(put(dy), tok, vocab, scale=0.75, dtype=grad)
+        within(got, ref, (ref.abs() * (2 * E + U[grad]) + mag * min(rows, 544) * E) * 1.001 + TINY[grad], "its gradient")
+
+        x = randn(base + 3, rows, hidden, dtype=dtype, mean=0.4)
+        w, b = randn(base + 4, hidden, mean=1.0, std=0.2, dtype=grad), randn(base + 5, hidden, dtype=grad)
+        ry, rm, rr, n = plain_norm(x, w, b, 1e-5)
+        y, mean, rstd = A.layer_norm(put(x), w, b)
+        bound, dn = norm_bounds(ry, n, w, b, dtype)
+        within(y, ry, bound, "norm")
+        within(rstd, rr, N_ERR * rr, "rstd")
+        yk, rk, nc, ns = A.layer_norm_keep(put(x), w, b)
+        assert torch.equal(yk, y) and torch.equal(rk, rstd)
+        c = chain(rows, hidden)
+        kept = A.checkpoint_unpack(nc, ns, F32)
+        step = torch.exp2(ns.double() - 128).repeat_interleave(32, 1)[:, :hidden]  # half a step of each block
+        within(kept, n, step + dn, "kept rows")
+        for got, nn in ((A.layer_norm_grad(put(dy), put(x), mean, rstd, w),
+                         (x.double() - mean.double()[:, None]) * rstd.double()[:, None]),
+                        (A.layer_norm_keep_grad(put(dy), nc, ns, rstd, w), kept.double())):
+            rx, rw, rb, mx, mw, mb = plain_norm_grad(dy, nn, rstd, w)
+            within(got[0], rx, mx + (U[dtype] + E) * rx.abs() + TINY[dtype], "dx")
+            within(got[1], rw, (c + 4) * E * mw + (E + U[grad]) * rw.abs() + TINY[grad], "dweight")
+            within(got[2], rb, c * E * mb + (E + U[grad]) * rb.abs() + TINY[grad], "dbias")
+
+        x = randn(base + 6, rows, hidden, dtype=dtype)
+        codes, scales = A.checkpoint_pack(put(x))
+        back = A.checkpoint_unpack(codes, scales, F32).double()
+        half = torch.exp2(scales.double() - 128).repeat_interleave(32, 1)[:, :hidden]
+        within(back, x.double(), half, "kept")
+        dz = randn(base + 7, rows, out, dtype=dtype)
+        bw, bb = linear_bound(dz, back, rows, dtype)
+        dw, db = A.linear_grad(put(dz), codes, scales, dtype=grad)
+        rw, rb = dz.double().t() @ back, dz.double().sum(0)
+        within(dw, rw, bw + (U[grad] + E) * rw.abs() + TINY[grad], "dweight of linear")
+        within(db, rb, bb + (U[grad] + E) * rb.abs() + TINY[grad], "dbias of linear")
+
+
 def test_workers_gradients_into_the_combine(gpu):
     """Four workers' microbatches through embedding, norm and a linear layer
     and back, in two accumulated halves, every gradient written into its
