@@ -13,6 +13,12 @@ must not overlap another argument.  The functions work on plain tensors and
 record no autograd graph.  ``stream=None`` is the current stream of the
 tensors' device; with a stream given, outputs and workspace are allocated on
 it, and inputs must stay alive until it has passed the call.
+
+``workspace``: a contiguous tensor of at least the bytes that the library's
+``adasum_..._workspace_bytes`` names, aligned to 16 bytes, for callers that
+keep one; calls that share it must follow each other on one stream, and graphs
+that share it must not run at the same time.  By default each call allocates
+its own.
 """
 
 import torch
