@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a, int nblk, uint32_
 template <typename T>
 __global__ __launch_bounds__(256) void unpack_kernel(UnpackArgs a, int nblk) {
   constexpr int VEC = Type<T>::kVec;
-  const uint32_t per_row = (uint32_t)((a.hidden + VEC - 1) / VEC);
+  const uint32_t per_row = ((uint32_t)a.hidden + VEC - 1) / VEC;  // a.hidden may be 2^31 - 1
   const int64_t total = a.rows * per_row;
   for (int64_t first = (int64_t)blockIdx.x * 256 * kPieces; first < total;
        first += (int64_t)gridDim.x * 256 * kPieces) {

@@ -1103,3 +1103,20 @@ def test_workers_gradients_into_the_combine(gpu):
         err = float(np.linalg.norm(a - c) / np.linalg.norm(c))
         flush_print(f"  segment {i}: relative L2 {err:.3g}")
         assert err <= 1e-5  # the combine's own tolerance; fp32 gradients are off by about 1e-6
+
+
+def test_widest_kept_row(gpu):
+    """A row of 2^31 - 1 values, packed and read back, like its first and last
+    blocks alone."""
+    width, end = 2 ** 31 - 1, 4096 + 31
+    x = torch.zeros(width, dtype=BF16, device="cuda")
+    x[:4096], x[-end:] = randn(200, 4096, dtype=BF16), randn(201, end, dtype=BF16)
+    flush_print("pack")
+    codes, scales = A.checkpoint_pack(x)
+    flush_print("unpack")
+    back = A.checkpoint_unpack(codes, scales, BF16)
+    for part, blocks in ((slice(0, 4096), slice(0, 128)), (slice(width - end, width), slice(-129, None))):
+        c, s = A.checkpoint_pack(x[part])
+        assert torch.equal(codes[part], c) and torch.equal(scales[blocks], s)
+        assert torch.equal(back[part], A.checkpoint_unpack(c, s, BF16))
+    assert not bool(back[4096:width - end].any()) and not bool(codes[4096:width - end].any())
