@@ -378,10 +378,14 @@ struct RunArgs {
   int64_t pitch;
 };
 
-// The grouped list as the summing kernels read it: whatever it holds, they
-// stay inside dy and grad.  It is right as long as the tokens do not change
-// between the grouping kernel's two scans; a caller that breaks this gets
-// wrong sums, not accesses out of bounds.
+// The grouped list as the summing kernels read it.  The bounds are a guard, not
+// part of the sum: versions of these kernels without them failed twice on the
+// GPU (a silent stop, an illegal access), no reading of the sources and no run
+// of them on the CPU showed why, and the list is the only thing read back that
+// becomes an address.  A wrong list, from that cause or from a caller that
+// changes the tokens during the call, would show as wrong sums and not as a
+// fault: an index out of range counts as row 0 or token 0.  So the tests
+// compare the list at every position, on the CPU and on the GPU.
 __device__ __forceinline__ int64_t listed_rows(const RunArgs& a) {
   const int64_t m = *a.count;
   return m < 0 ? 0 : m < a.n ? m : a.n;

@@ -58,3 +58,25 @@ def run(exe, *args):
 def test_checkpoint(program):
     """Packing and reading back, and the pieces of a row of 2^31 - 1 values."""
     run(program("checkpoint"))
+
+
+UNIFORM, HALF, ONE, NONE, OUTSIDE, FALLING = range(6)
+F32, F16, BF16 = range(3)
+
+
+@pytest.mark.parametrize("n,vocab,hidden,kind,dtype,grad,token_bytes,accumulate", [
+    (1, 1, 1, UNIFORM, F32, F32, 8, 0),
+    (700, 40, 33, OUTSIDE, BF16, F32, 4, 0),
+    (700, 40, 33, HALF, F16, F16, 8, 1),
+    (3000, 3, 8, UNIFORM, F32, BF16, 8, 0),
+    (9000, 1, 16, ONE, BF16, BF16, 4, 0),
+    (9000, 5, 7, FALLING, F32, F32, 8, 1),
+    (2000, 60, 20, NONE, F32, F32, 8, 0),
+    (2000, 140000, 5, UNIFORM, BF16, F32, 8, 0),
+    (25000, 5000, 1031, UNIFORM, F32, F32, 8, 0),
+    (25000, 5000, 1031, HALF, BF16, F32, 4, 1),
+    (65536, 30522, 1024, FALLING, BF16, F32, 8, 0),
+])
+def test_embedding_grad(program, n, vocab, hidden, kind, dtype, grad, token_bytes, accumulate):
+    """The grouped list is right at every position and the sums are exact."""
+    run(program("embedding"), n, vocab, hidden, kind, dtype, grad, token_bytes, accumulate)

@@ -1120,3 +1120,37 @@ def test_widest_kept_row(gpu):
         assert torch.equal(codes[part], c) and torch.equal(scales[blocks], s)
         assert torch.equal(back[part], A.checkpoint_unpack(c, s, BF16))
     assert not bool(back[4096:width - end].any()) and not bool(codes[4096:width - end].any())
+
+
+@pytest.mark.parametrize("n,vocab,hidden,kind", [(3000, 700, 40, "outside"), (70000, 30, 16, "frequent"),
+                                                 (25000, 5000, 1031, "uniform"), (65536, 30522, 64, "falling"),
+                                                 (9000, 140000, 8, "uniform"), (40000, 1, 4, "one")])
+def test_embedding_grad_list(gpu, n, vocab, hidden, kind):
+    """The grouped list that the embedding gradient leaves in its workspace
+    (int32 rows, int32 tokens, their number, each from a multiple of 256
+    bytes) is right at every position, so no bound of its readers is met."""
+    flush_print(f"embedding_grad list n={n} vocab={vocab} {kind}")
+    if kind == "falling":
+        rank = torch.exp(torch.rand(n, generator=gen(210), dtype=torch.float64) * math.log(vocab + 1)).long()
+        t = torch.where(torch.rand(n, generator=gen(211)) < 0.1, -1, rank.clamp(1, vocab) - 1).cuda()
+    else:
+        t = tokens_of(210, n, vocab, kind)
+    groups = 256  # the workgroup a token belongs to is its low bits
+    while groups > 1 and groups // 2 >= vocab:
+        groups //= 2
+    while -(-vocab // groups) > 512:
+        groups *= 2
+    host = t.cpu().numpy()
+    rows = np.nonzero((host >= 0) & (host < vocab))[0]
+    rows = rows[np.lexsort((rows, host[rows] // groups, host[rows] % groups))]
+    need = _native.lib().adasum_embedding_grad_workspace_bytes(n, hidden, 0)
+    ws = torch.full((need,), 0x55, dtype=torch.uint8, device="cuda")
+    dy = randn(212, n, hidden)
+    for tok in (t, t.to(torch.int32)):
+        ws.fill_(0x55)
+        A.embedding_grad(dy, tok, vocab, workspace=ws)
+        w = ws.cpu().numpy()
+        at = -(-4 * n // 256) * 256
+        assert w[2 * at:2 * at + 4].view(np.int32)[0] == len(rows)
+        assert np.array_equal(w[:4 * len(rows)].view(np.int32), rows)
+        assert np.array_equal(w[at:at + 4 * len(rows)].view(np.int32), host[rows])
