@@ -283,7 +283,7 @@ def layer_norm_keep(x, weight=None, bias=None, *, eps=1e-5, out=None, stream=Non
     return _norm(x, weight, bias, eps, out, stream, True)
 
 
-def _norm_grad(dy, x, mean, codes, scales, rstd, weight, dx, dweight, dbias, accumulate, workspace, stream):
+def _norm_grad(dy, x, mean, codes, scales, rstd, weight, dx, dweight, dbias, bias, accumulate, workspace, stream):
     dev = _on(dy, "dy").device
     rows, hidden, stride = _rows(dy, "dy")
     code = _code(dy.dtype, "dy")
@@ -302,32 +302,32 @@ def _norm_grad(dy, x, mean, codes, scales, rstd, weight, dx, dweight, dbias, acc
     if dx is not None:
         _like(dx, "dx", dev, dy.shape, dy.dtype)
         dx_stride = _rows(dx, "dx")[2]
-    if accumulate and (weight is None or dweight is None or dbias is None):
-        raise ValueError("accumulate needs weight, dweight and dbias")
-    grad_dtype = weight.dtype if weight is not None else torch.float32
-    if weight is None:
-        if dweight is not None or dbias is not None:
-            raise ValueError("a norm without weight has no dweight and dbias")
-    else:
-        given = [t.dtype for t in (dweight, dbias) if t is not None]
-        if given:
-            grad_dtype = given[0]
-        for t, name in ((dweight, "dweight"), (dbias, "dbias")):
-            if t is not None:
-                _dense(t, name, dev, (hidden,), grad_dtype)
+    if weight is None and dweight is not None:
+        raise ValueError("a norm without weight has no dweight")
+    want_weight = weight is not None
+    want_bias = dbias is not None or (want_weight if bias is None else bool(bias))
+    if accumulate and (not (want_weight or want_bias) or (want_weight and dweight is None) or
+                       (want_bias and dbias is None)):
+        raise ValueError("accumulate needs dweight for a weight, and dbias unless bias is False")
+    given = [t.dtype for t in (dweight, dbias) if t is not None]
+    grad_dtype = given[0] if given else weight.dtype if want_weight else torch.float32
+    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is not None:
+            _dense(t, name, dev, (hidden,), grad_dtype)
     grad_code = _code(grad_dtype, "dweight")
     L = _native.lib()
     need = 0
-    if weight is not None:
+    if want_weight or want_bias:
         need = _native.check(L.adasum_layer_norm_grad_workspace_bytes(rows, hidden, code))
 
     def body(st):
         ws = _workspace(workspace, need, dev)
         d = _fresh(dy, dy.dtype) if dx is None else dx
         dw, db = dweight, dbias
-        if weight is not None:
-            dw = torch.empty(hidden, dtype=grad_dtype, device=dev) if dw is None else dw
-            db = torch.empty(hidden, dtype=grad_dtype, device=dev) if db is None else db
+        if want_weight and dw is None:
+            dw = torch.empty(hidden, dtype=grad_dtype, device=dev)
+        if want_bias and db is None:
+            db = torch.empty(hidden, dtype=grad_dtype, device=dev)
         _native.check(L.adasum_layer_norm_grad(
             dy.data_ptr(), rows, hidden, stride, code, _ptr(x), x_stride, _ptr(mean), _ptr(codes), _ptr(scales),
             rstd.data_ptr(), _ptr(weight), param_code, d.data_ptr(), dx_stride, _ptr(dw), _ptr(db), grad_code,
@@ -336,25 +336,27 @@ def _norm_grad(dy, x, mean, codes, scales, rstd, weight, dx, dweight, dbias, acc
     return _call(dev, stream, body)
 
 
-def layer_norm_grad(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=None, accumulate=False,
-                    workspace=None, stream=None):
-    """Backward pass of :func:`layer_norm`: (dx, dweight, dbias); the last two
-    None for a norm without weight.
+def layer_norm_grad(dy, x, mean, rstd, weight=None, *, dx=None, dweight=None, dbias=None, bias=None,
+                    accumulate=False, workspace=None, stream=None):
+    """Backward pass of :func:`layer_norm`: (dx, dweight, dbias); dweight None
+    for a norm without weight.
 
-    dx has the dtype of dy and x; dweight and dbias that of weight, or of the
-    tensors given for them (segments of a gradient buffer), to which they are
-    added with accumulate.
+    bias: whether dbias is wanted (else None); by default with a weight, or
+    where a tensor is given for it.  dx has the dtype of dy and x; dweight and
+    dbias that of weight (fp32 without one), or of the tensors given for them
+    (segments of a gradient buffer), to which they are added with accumulate.
     """
     if x is None or mean is None:
         raise ValueError("x and mean are needed; with kept rows use layer_norm_keep_grad")
-    return _norm_grad(dy, x, mean, None, None, rstd, weight, dx, dweight, dbias, accumulate, workspace, stream)
+    return _norm_grad(dy, x, mean, None, None, rstd, weight, dx, dweight, dbias, bias, accumulate, workspace, stream)
 
 
-def layer_norm_keep_grad(dy, codes, scales, rstd, weight=None, *, dx=None, dweight=None, dbias=None,
+def layer_norm_keep_grad(dy, codes, scales, rstd, weight=None, *, dx=None, dweight=None, dbias=None, bias=None,
                          accumulate=False, workspace=None, stream=None):
     """Backward pass of :func:`layer_norm_keep`, from the rows kept in 8 bits;
     arguments and results as for :func:`layer_norm_grad`."""
-    return _norm_grad(dy, None, None, codes, scales, rstd, weight, dx, dweight, dbias, accumulate, workspace, stream)
+    return _norm_grad(dy, None, None, codes, scales, rstd, weight, dx, dweight, dbias, bias, accumulate, workspace,
+                      stream)
 
 
 def checkpoint_pack(x, *, codes=None, scales=None, stream=None):

@@ -1154,3 +1154,50 @@ def test_embedding_grad_list(gpu, n, vocab, hidden, kind):
         assert w[2 * at:2 * at + 4].view(np.int32)[0] == len(rows)
         assert np.array_equal(w[:4 * len(rows)].view(np.int32), rows)
         assert np.array_equal(w[at:at + 4 * len(rows)].view(np.int32), host[rows])
+
+
+@pytest.mark.parametrize("kept", [False, True], ids=["x", "kept"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_layer_norm_grad_of_one_parameter(gpu, dtype, kept):
+    """A norm with a bias alone and one with a weight alone: the gradient of
+    the parameter that is there, asked for, given a segment, and added to."""
+    rows, hidden = 90, 77
+    x, dy = randn(220, rows, hidden, dtype=dtype), randn(221, rows, hidden, dtype=dtype)
+    w, b = randn(222, hidden, dtype=dtype), randn(223, hidden, dtype=dtype)
+
+    def back(weight, **kw):
+        if kept:
+            _, rstd, codes, scales = A.layer_norm_keep(x, weight, b if weight is None else None)
+            return A.layer_norm_keep_grad(dy, codes, scales, rstd, weight, **kw)
+        _, mean, rstd = A.layer_norm(x, weight, b if weight is None else None)
+        return A.layer_norm_grad(dy, x, mean, rstd, weight, **kw)
+
+    both, none = back(w), back(None)
+    assert none[1] is None and none[2] is None
+    dx, no, db = back(None, bias=True)
+    assert no is None and db.dtype == F32 and same([dx], [none[0]])
+    # the sums of dy are those of a norm with both parameters
+    assert torch.equal(db.to(dtype), both[2])
+    seg = torch.full((hidden + 6,), 1.5, dtype=dtype, device="cuda")
+    got = back(None, dbias=seg[3:3 + hidden])
+    assert got[1] is None and got[2].data_ptr() == seg[3:].data_ptr() and torch.equal(got[2], both[2])
+    first = got[2].double().clone()
+    back(None, dbias=got[2], accumulate=True)
+    want = first + dy.double().sum(0)
+    mag = dy.double().abs().sum(0)
+    within(got[2], want, chain(rows, hidden) * E * mag + (U[dtype] + E) * want.abs() + TINY[dtype], "dbias added")
+    assert bool((seg[:3] == 1.5).all()) and bool((seg[-3:] == 1.5).all())
+
+    dx, dw, no = back(w, bias=False)
+    assert no is None and same([dx, dw], both[:2])
+    twice = [dw.clone(), both[1].clone(), both[2].clone()]
+    back(w, dweight=twice[0], bias=False, accumulate=True)
+    back(w, dweight=twice[1], dbias=twice[2], accumulate=True)
+    assert torch.equal(twice[0], twice[1])
+    for bad in (dict(accumulate=True), dict(bias=True, accumulate=True), dict(bias=False, accumulate=True)):
+        with pytest.raises(ValueError):
+            back(None, **bad)
+        with pytest.raises(ValueError):
+            back(w, **bad)
+    with pytest.raises(ValueError):
+        back(None, dweight=w.clone(), bias=True)
