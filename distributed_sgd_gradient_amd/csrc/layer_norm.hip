@@ -413,8 +413,11 @@ int norm_grad_blocks(int64_t rows, int hidden) {
   // one per CU at least; and no more than leaves a wave four rows, or 16 lanes
   // two: every workgroup leaves a row of partial sums for the join.  65536 x
   // 1024 bf16: 75 us whether 512 or 1024 workgroups, the join 5 against 8 us.
-  return (int)std::min<int64_t>(ceil_div(rows, s.rows * (s.lanes == 16 ? 2 : 4)),
-                                std::max<int64_t>(kCUs, (int64_t)kCUs * 512 / s.threads));
+  const int64_t blocks = std::min<int64_t>(ceil_div(rows, s.rows * (s.lanes == 16 ? 2 : 4)),
+                                           std::max<int64_t>(kCUs, (int64_t)kCUs * 512 / s.threads));
+  // Many rows take more workgroups than run at once, so that the fp32 sums of
+  // dweight and dbias stay kNormGradRows long.
+  return (int)std::max<int64_t>(blocks, ceil_div(rows, (int64_t)s.rows * kNormGradRows));
 }
 
 hipError_t launch_norm_grad(int dtype, const NormGradArgs& a, hipStream_t st) {

@@ -16,6 +16,7 @@ namespace adasum {
 constexpr int kCUs = 256;                 // compute units of an MI355X
 constexpr int kScaleBlock = 32;           // values that share an 8-bit scale
 constexpr int kMaxNormHidden = 16384;     // widest row of the layer norm kernels (held in registers)
+constexpr int kNormGradRows = 1024;       // rows that one fp32 sum of the layer norm gradient takes at most
 constexpr int64_t kMaxDim = int64_t(1) << 31;  // rows, tokens, vocabulary and widths stay below this
 constexpr int64_t kMaxEmbeddingHidden = int64_t(1) << 23;  // a launch has 65536 workgroups along a row at most
 // Row stride of the linear gradient's dy: a row's offset is the product of two

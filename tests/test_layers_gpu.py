@@ -1201,3 +1201,20 @@ def test_layer_norm_grad_of_one_parameter(gpu, dtype, kept):
             back(w, **bad)
     with pytest.raises(ValueError):
         back(None, dweight=w.clone(), bias=True)
+
+
+def test_layer_norm_grad_sums_are_bounded(gpu):
+    """Equal terms d = 1 + 2^-11 - 2^-23: a running fp32 sum loses 2^-11 with
+    every term from 2^13 on, 2^-12 of the whole at 2^14 terms.  However many
+    rows there are, a sum takes at most 1024, then two steps across the wave
+    and three other waves, and the rest is added in fp64: 1029 roundings."""
+    rows, d = 1 << 27, 1 + 2.0 ** -11 - 2.0 ** -23
+    dy = torch.full((rows, 2), d, device="cuda")
+    one, w = torch.ones(rows, device="cuda"), torch.ones(2, device="cuda")
+    codes = torch.full((rows, 2), 64, dtype=torch.int8, device="cuda")
+    scales = torch.full((rows, 1), 121, dtype=torch.uint8, device="cuda")  # 64 * 2^-6
+    for dx, dw, db in (A.layer_norm_keep_grad(dy, codes, scales, one, w),
+                       A.layer_norm_grad(dy, codes.to(F32), torch.full_like(one, 63.0), one, w)):
+        for got, what in ((dw, "dweight"), (db, "dbias")):
+            within(got, torch.full((2,), rows * d, dtype=torch.float64), 1030 * E * rows * d, what)
+        del dx

@@ -196,3 +196,12 @@ def test_every_layer_entry_point_is_covered():
     for name in CALLS:
         assert len(CALLS[name]) == len(_native.SIGNATURES[name][1])
         assert _native.SIGNATURES[name][0] is ctypes.c_int
+
+
+@pytest.mark.parametrize("rows,hidden,together", [(1 << 27, 2, 16), (1 << 24, 256, 16), (1 << 24, 1000, 4),
+                                                  (1 << 22, 4000, 1), (1 << 20, 16384, 1)])
+def test_layer_norm_grad_sums_are_bounded(rows, hidden, together):
+    """A partial sum of dweight and dbias for every 1024 rows of each of the
+    `together` rows that a workgroup takes at a time."""
+    parts = -(-rows // (1024 * together))
+    assert _native.lib().adasum_layer_norm_grad_workspace_bytes(rows, hidden, F32) >= parts * 2 * hidden * 4
