@@ -407,30 +407,60 @@ hipError_t launch_norm(int dtype, const NormArgs& a, hipStream_t st) {
   return with_dtype(dtype, [&](auto t) { return norm_width<decltype(t)>(a, st); });
 }
 
-int norm_grad_blocks(int64_t rows, int hidden) {
-  const GradShape s = grad_shape(hidden);
+namespace {
+
+// Workgroups of one launch over `rows`.
+int grad_blocks(int64_t rows, const GradShape& s) {
   // Two workgroups of 256 lanes per CU, or as many waves in wider ones, but
   // one per CU at least; and no more than leaves a wave four rows, or 16 lanes
   // two: every workgroup leaves a row of partial sums for the join.  65536 x
   // 1024 bf16: 75 us whether 512 or 1024 workgroups, the join 5 against 8 us.
-  const int64_t blocks = std::min<int64_t>(ceil_div(rows, s.rows * (s.lanes == 16 ? 2 : 4)),
-                                           std::max<int64_t>(kCUs, (int64_t)kCUs * 512 / s.threads));
-  // Many rows take more workgroups than run at once, so that the fp32 sums of
-  // dweight and dbias stay kNormGradRows long.
-  return (int)std::max<int64_t>(blocks, ceil_div(rows, (int64_t)s.rows * kNormGradRows));
+  return (int)std::min<int64_t>(ceil_div(rows, s.rows * (s.lanes == 16 ? 2 : 4)),
+                                std::max<int64_t>(kCUs, (int64_t)kCUs * 512 / s.threads));
+}
+
+// Rows of one launch: as many as leave the fp32 sums of dweight and dbias
+// kNormGradRows long in a full one.  (More workgroups in one launch instead:
+// 1048576 x 4096 bf16 5450 us against 4900.)
+int64_t grad_rows(const GradShape& s) {
+  return (int64_t)grad_blocks(kMaxDim, s) * s.rows * kNormGradRows;
+}
+
+}  // namespace
+
+int64_t norm_grad_parts(int64_t rows, int hidden) {
+  const GradShape s = grad_shape(hidden);
+  const int64_t full = grad_rows(s);
+  return rows / full * grad_blocks(full, s) + grad_blocks(rows % full, s);
 }
 
 hipError_t launch_norm_grad(int dtype, const NormGradArgs& a, hipStream_t st) {
   const GradShape s = grad_shape(a.hidden);
-  const int blocks = a.rows > 0 ? norm_grad_blocks(a.rows, a.hidden) : 0;
-  if (blocks > 0) {
+  const int64_t full = grad_rows(s), size = dtype == 0 ? 4 : 2;
+  int64_t parts = 0;
+  for (int64_t first = 0; first < a.rows; first += full) {
+    NormGradArgs b = a;
+    b.rows = std::min(full, a.rows - first);
+    b.dy = static_cast<const char*>(a.dy) + first * a.dy_stride * size;
+    b.dx = static_cast<char*>(a.dx) + first * a.dx_stride * size;
+    b.rstd = a.rstd + first;
+    if (a.x) {
+      b.x = static_cast<const char*>(a.x) + first * a.x_stride * size;
+      b.mean = a.mean + first;
+    } else {
+      b.codes = a.codes + first * a.hidden;
+      b.scales = a.scales + first * ceil_div(a.hidden, kScaleBlock);
+    }
+    if (a.partials) b.partials = a.partials + parts * 2 * a.hidden;
+    const int blocks = grad_blocks(b.rows, s);
+    parts += blocks;
     const hipError_t e =
-        with_dtype(dtype, [&](auto t) { return norm_grad_width<decltype(t)>(a, s.lanes, blocks, st); });
+        with_dtype(dtype, [&](auto t) { return norm_grad_width<decltype(t)>(b, s.lanes, blocks, st); });
     if (e != hipSuccess) return e;
   }
   if (a.dweight || a.dbias) {
     const int64_t cols = 2 * (int64_t)a.hidden;
-    norm_grad_join_kernel<<<(unsigned)ceil_div(cols, 32), 256, 0, st>>>(a.partials, blocks, a.hidden, a.dweight,
+    norm_grad_join_kernel<<<(unsigned)ceil_div(cols, 32), 256, 0, st>>>(a.partials, (int)parts, a.hidden, a.dweight,
                                                                       a.dbias, a.grad_dtype, a.accumulate);
     return hipGetLastError();
   }

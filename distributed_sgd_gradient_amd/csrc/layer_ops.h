@@ -69,10 +69,11 @@ struct NormGradArgs {
   void* dbias;          // NULL: not wanted
   int grad_dtype;
   int accumulate;
-  float* partials;      // norm_grad_blocks(...) x 2 x hidden
+  float* partials;      // norm_grad_parts(...) x 2 x hidden
 };
-// Workgroups of the backward pass, each with a row of partial sums.
-int norm_grad_blocks(int64_t rows, int hidden);
+// Workgroups of the backward pass (in one launch or more), each with a row of
+// partial sums.
+int64_t norm_grad_parts(int64_t rows, int hidden);
 hipError_t launch_norm_grad(int dtype, const NormGradArgs& a, hipStream_t st);
 
 // ---------------------------------------------------------------- 8-bit activations

@@ -250,7 +250,7 @@ int layer_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, in
 }
 
 size_t norm_grad_workspace(int64_t rows, int64_t hidden) {
-  return rows == 0 ? 0 : (size_t)norm_grad_blocks(rows, (int)hidden) * 2 * hidden * sizeof(float);
+  return rows == 0 ? 0 : (size_t)norm_grad_parts(rows, (int)hidden) * 2 * hidden * sizeof(float);
 }
 
 int64_t layer_norm_grad_bytes(int64_t rows, int64_t hidden, int dtype) {
