@@ -19,6 +19,10 @@ constexpr int kMaxNormHidden = 16384;     // widest row of the layer norm kernel
 constexpr int kNormGradRows = 1024;       // rows that one fp32 sum of the layer norm gradient takes at most
 constexpr int64_t kMaxDim = int64_t(1) << 31;  // rows, tokens, vocabulary and widths stay below this
 constexpr int64_t kMaxEmbeddingHidden = int64_t(1) << 23;  // a launch has 65536 workgroups along a row at most
+// Rows that one fp32 sum of the linear gradient takes at most.  A split more of
+// a dweight too large to be split otherwise costs the writing and reading of
+// its partial sums, 8 bytes beside the 131072 operations of each.
+constexpr int64_t kMaxLinearRows = 65536;
 // Row stride of the linear gradient's dy: a row's offset is the product of two
 // 32-bit numbers, the row and the stride in bytes.
 constexpr int64_t kMaxLinearStride = int64_t(1) << 28;

@@ -14,7 +14,8 @@
 // is a bf16 value, and an fp16 value too where fp16 activations were packed.
 // So 16-bit dy meets x in its own type; fp32 dy is cut into three bf16 parts
 // of 8 bits each, hi + mid + lo = dy exactly, that meet x one after another.
-// Sums are fp32 within a split of the rows; splits are joined in fp64.
+// Sums are fp32 within a split of the rows, of at most 65536; splits are joined
+// in fp64.
 //
 // Bound by the matrix cores and what shares a CU with them: of 65536 x 4096 x
 // 1024 in bf16, 485 to 508 us in all on different cards (1080 to 1130 TFLOP/s;
@@ -505,6 +506,8 @@ LinearGradLayout linear_grad_layout(int64_t rows, int64_t out, int64_t in, int d
       best = s;
     }
   }
+  // and no fp32 sum longer than kMaxLinearRows
+  best = std::max(best, ceil_div(steps, kMaxLinearRows / kStep));
   l.split_rows = ceil_div(steps, best) * kStep;
   l.splits = (int)std::max<int64_t>(1, ceil_div(rows, l.split_rows));
   size_t at = 0;

@@ -221,7 +221,8 @@ ADASUM_API int64_t adasum_sum_workspace_bytes(int K, int64_t N, int dtype);
  *     element.
  *   - dtype, param_dtype, grad_dtype, ... are adasum_dtype_t.  Arithmetic is
  *     fp32, results are rounded once to nearest even; sums over rows are fp32
- *     in pieces of bounded length, joined in fp64.
+ *     in pieces of at most 2048 rows (embedding), 16384 (layer norm) or 65536
+ *     (linear), joined in fp64.
  *   - accumulate != 0 adds the gradient to what dweight, dbias or grad holds
  *     (the microbatches of one step) instead of replacing it.
  *   - Zero rows (or tokens) are allowed: gradients are then zero (unchanged

@@ -1218,3 +1218,19 @@ def test_layer_norm_grad_sums_are_bounded(gpu):
         for got, what in ((dw, "dweight"), (db, "dbias")):
             within(got, torch.full((2,), rows * d, dtype=torch.float64), 1030 * E * rows * d, what)
         del dx
+
+
+def test_linear_grad_sums_are_bounded(gpu):
+    """A dweight of so many tiles that its rows are split for the length of
+    the sums alone: within the bound of 65536 rows, four times as many."""
+    base, out, width, times = 4096, 1024, 16384, 64
+    flush_print(f"linear_grad rows={base * times} out={out} in={width}")
+    dy, codes, scales, x = linear_case(230, base, out, width, F32)
+    rw, rb = times * (dy.double().t() @ x), times * dy.double().sum(0)
+    bw, bb = linear_bound(dy, x, base, F32)
+    per = 65536 // base  # linear_bound of 65536 rows, from the steps of `base`
+    steps = base // 32 * 3 + 2
+    bw, bb = bw / steps * (steps * per) * times, times * dy.double().abs().sum(0) * (65536 / 4 + 12) * E
+    dw, db = A.linear_grad(dy.repeat(times, 1), codes.repeat(times, 1), scales.repeat(times, 1))
+    within(dw, rw, bw + 2 * E * rw.abs(), "dweight")
+    within(db, rb, bb + 2 * E * rb.abs(), "dbias")

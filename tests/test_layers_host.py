@@ -205,3 +205,12 @@ def test_layer_norm_grad_sums_are_bounded(rows, hidden, together):
     `together` rows that a workgroup takes at a time."""
     parts = -(-rows // (1024 * together))
     assert _native.lib().adasum_layer_norm_grad_workspace_bytes(rows, hidden, F32) >= parts * 2 * hidden * 4
+
+
+@pytest.mark.parametrize("rows,out,width,dtype", [(1 << 20, 30522, 1024, BF16), (65537, 32768, 1024, F16),
+                                                  (1 << 18, 1024, 16384, F32)])
+def test_linear_grad_sums_are_bounded(rows, out, width, dtype):
+    """A partial sum of dweight for every 65536 rows."""
+    parts = -(-rows // 65536)
+    assert parts > 1
+    assert _native.lib().adasum_linear_grad_workspace_bytes(rows, out, width, dtype) >= parts * out * width * 4
