@@ -365,7 +365,9 @@ def checkpoint_pack(x, *, codes=None, scales=None, stream=None):
 
     32 consecutive values of a row share a power of two: value = code *
     2^(scale - 127).  A value is off by at most 1/127 of its block's largest
-    magnitude; a block that holds an infinity or NaN reads back as NaNs.
+    magnitude (or 2^-128); a block that holds an infinity or NaN reads back as
+    NaNs.  Gradients formed from kept rows are off accordingly: for normally
+    distributed rows 0.8 % of the norm of a dweight.
     """
     dev = _on(x, "x").device
     rows, width, stride = _rows(x, "x")

@@ -317,11 +317,16 @@ ADASUM_API int adasum_layer_norm_grad(const void* dy, int64_t rows, int64_t hidd
  * 32 consecutive values of a row (fewer at its end) share a power of two:
  * value = codes[r][c] * 2^(scales[r][c / 32] - 127), codes in [-127, 127].
  * The power is the least with 127 steps reaching the block's largest
- * magnitude, and codes are rounded to nearest even, so a value is off by at
- * most half a step, 1/127 of the block's largest magnitude.  Steps are at
- * least 2^-127, and at most 2^121 (2^9 for fp16), so that no value rounds up
- * to an infinity.  A block that holds an infinity or NaN has scale 255 and
- * reads back as NaNs.
+ * magnitude, but at least 2^-127, and at most 2^121 (2^9 for fp16), so that no
+ * value rounds up to an infinity.  Codes are rounded to nearest even, those
+ * past 127 of the largest steps to 127.  A value is off by at most d = 1/127 of
+ * its block's largest magnitude (or 2^-128, half the least step); a block that
+ * holds an infinity or NaN has scale 255 and reads back as NaNs.
+ *
+ * So a gradient formed from kept rows is off from that of the rows themselves
+ * by up to the sum of |dy| d over the rows (dweight), and by r (d |<g n>| +
+ * |n| <|g| d>) in the dx of a layer norm.  Of normally distributed rows: 0.8 %
+ * of dweight's norm, 0.07 % of dx's.
  *
  *   x, out       rows x hidden elements of dtype.
  *   codes        dense, rows x hidden.

@@ -1234,3 +1234,46 @@ def test_linear_grad_sums_are_bounded(gpu):
     dw, db = A.linear_grad(dy.repeat(times, 1), codes.repeat(times, 1), scales.repeat(times, 1))
     within(dw, rw, bw + 2 * E * rw.abs(), "dweight")
     within(db, rb, bb + 2 * E * rb.abs(), "dbias")
+
+
+def block_error(x):
+    """What keeping rows x in 8 bits may cost each value: 1/127 of its block's
+    largest magnitude, and half of the least step."""
+    rows, width = x.shape
+    wide = torch.zeros(rows, -(-width // 32) * 32, dtype=torch.float64, device=x.device)
+    wide[:, :width] = x.double().abs()
+    return wide.view(rows, -1, 32).amax(2).repeat_interleave(32, 1)[:, :width] / 127 + 2.0 ** -128
+
+
+def relative(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_what_8_bits_cost_the_gradients(gpu, dtype):
+    """The gradients from kept rows against those of the layers that ran, of
+    the unrounded rows, within what the rounding of each value may cost."""
+    rows, hidden, out = 2000, 264, 72
+    x, w = randn(240, rows, hidden, dtype=dtype, mean=0.3), randn(241, hidden, mean=1.0, std=0.2)
+    dy = randn(242, rows, hidden, dtype=dtype)
+    _, rstd, codes, scales = A.layer_norm_keep(x, w)
+    _, _, _, n = plain_norm(x, None, None, 1e-5)
+    dn = block_error(n) + N_ERR * (n.abs() + 1)
+    dx, dw, db = A.layer_norm_keep_grad(dy, codes, scales, rstd, w)
+    rx, rw, rb, mx, mw, mb = plain_norm_grad(dy, n, rstd, w)
+    # k the kept row, n the true one: dx differs by r ((k - n) <g k> + n <g (k - n)>)
+    g, r = dy.double() * w.double(), rstd.double()[:, None]
+    k = A.checkpoint_unpack(codes, scales).double()
+    off = r * (dn * (g * k).mean(1, keepdim=True).abs() + n.abs() * (g.abs() * dn).mean(1, keepdim=True))
+    within(dx, rx, 1.02 * mx + off + (U[dtype] + 2 * E) * (rx.abs() + off) + TINY[dtype], "dx")
+    c = chain(rows, hidden)
+    within(dw, rw, (c + 5) * E * 1.02 * mw + (dy.double().abs() * dn).sum(0), "dweight")
+    within(db, rb, c * E * mb + E * rb.abs(), "dbias")
+    flush_print(f"  relative to the layer's own gradient: dx {relative(dx, rx):.2g}, dweight {relative(dw, rw):.2g}")
+    dz = randn(243, rows, out, dtype=dtype)
+    codes, scales = A.checkpoint_pack(x)
+    dw, _ = A.linear_grad(dz, codes, scales, dtype=F32)
+    want = dz.double().t() @ x.double()
+    bw, _ = linear_bound(dz, A.checkpoint_unpack(codes, scales).double(), rows, dtype)
+    within(dw, want, bw + dz.double().abs().t() @ block_error(x) + E * want.abs(), "dweight of linear")
+    flush_print(f"  dweight of linear {relative(dw, want):.2g}")
