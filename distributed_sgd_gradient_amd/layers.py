@@ -411,7 +411,10 @@ def linear_grad(dy, codes, scales, *, dtype=None, dweight=None, dbias=None, bias
     (dweight [out, in], dbias [out]); dbias None without bias.
 
     dy: [..., out]; codes, scales: x as :func:`checkpoint_pack` gives it, of
-    dy's dtype and leading shape.  dtype: of the gradients (default: dy's).
+    dy's dtype and leading shape.  Codes carry no type: with an fp16 dy, values
+    packed from another type (:func:`layer_norm_keep`'s are fp32 values) become
+    infinities above 65504 and are off by up to 2^-25 if they have bits below
+    2^-24.  dtype: of the gradients (default: dy's).
     dweight, dbias: contiguous tensors of out * in and out elements, for
     instance segments of a gradient buffer; with accumulate the gradients are
     added to them.

@@ -346,8 +346,12 @@ ADASUM_API int adasum_checkpoint_unpack(const int8_t* codes, const uint8_t* scal
  *
  *   dy           rows x out_features elements of dtype; dy_stride <= 2^28
  *                (of two rows or more).
- *   codes, scales rows x in_features activations packed from dtype (fp16:
- *                their values must be fp16 values, as packed ones are).
+ *   codes, scales rows x in_features activations packed from dtype.  Codes
+ *                carry no type, so this is not checked: values packed from
+ *                another type (those that adasum_layer_norm keeps are fp32
+ *                values whatever dtype is) are taken by fp32 and bf16 as they
+ *                are, by fp16 rounded to fp16: to an infinity above 65504,
+ *                off by up to 2^-25 where they have bits below 2^-24.
  *   dweight      dense, out_features x in_features elements of grad_dtype.
  *   dbias        out_features elements of grad_dtype; NULL: not wanted.
  *   workspace    adasum_linear_grad_workspace_bytes(...) bytes.

@@ -1277,3 +1277,29 @@ def test_what_8_bits_cost_the_gradients(gpu, dtype):
     bw, _ = linear_bound(dz, A.checkpoint_unpack(codes, scales).double(), rows, dtype)
     within(dw, want, bw + dz.double().abs().t() @ block_error(x) + E * want.abs(), "dweight of linear")
     flush_print(f"  dweight of linear {relative(dw, want):.2g}")
+
+
+def test_linear_grad_of_codes_of_another_type(gpu):
+    """fp16 products need fp16 values of x: codes packed from fp32 that are
+    not show as infinities or NaN where they are too large, and cost half of
+    fp16's least step, 2^-25, each where they are too small."""
+    rows, out, width = 300, 40, 96
+    x = randn(260, rows, width)
+    x[:, :32] *= 1e6
+    x[:, 32:64] *= 2.0 ** -20
+    codes, scales = A.checkpoint_pack(x)
+    dy = randn(261, rows, out, dtype=F16)
+    dw, _ = A.linear_grad(dy, codes, scales, dtype=F32)
+    assert not bool(torch.isfinite(dw[:, :32]).any())
+    back = A.checkpoint_unpack(codes, scales).double()[:, 32:]
+    want = dy.double().t() @ back
+    bw, _ = linear_bound(dy, back, rows, F16)
+    small = dy.double().abs().sum(0)[:, None] * 2.0 ** -25
+    within(dw[:, 32:], want, bw + 1.001 * small + E * want.abs(), "dweight")
+    assert float((dw[:, 32:64].double() - want[:, :32]).abs().max()) > 0  # which bf16 and fp32 do not lose
+    for dtype in (BF16, F32):
+        dw, _ = A.linear_grad(dy.to(dtype), codes, scales, dtype=F32)
+        back = A.checkpoint_unpack(codes, scales).double()
+        bw, _ = linear_bound(dy.to(dtype), back, rows, dtype)
+        want = dy.to(dtype).double().t() @ back
+        within(dw, want, bw + 2 * E * want.abs(), f"dweight {dtype}")
