@@ -1279,6 +1279,48 @@ def test_what_8_bits_cost_the_gradients(gpu, dtype):
     flush_print(f"  dweight of linear {relative(dw, want):.2g}")
 
 
+@pytest.mark.parametrize("rows,hidden,dtype", [(20001, 40, BF16), (20003, 128, F32), (9001, 250, F16),
+                                               (6001, 700, BF16), (1500, 4000, F16), (700, 9000, F32),
+                                               (1030, 16384, BF16), (600, 16383, F32)])
+def test_layer_norm_keep_grad_many_rows(gpu, rows, hidden, dtype):
+    """Several kept rows for every group of lanes, at each width that is
+    treated in its own way."""
+    x, dy = randn(250, rows, hidden, dtype=dtype, mean=0.3), randn(251, rows, hidden, dtype=dtype)
+    w = randn(252, hidden, mean=1.0, std=0.3)
+    flush_print(f"layer_norm_keep_grad rows={rows} hidden={hidden} {dtype}")
+    _, rstd, codes, scales = A.layer_norm_keep(x, w)
+    n = A.checkpoint_unpack(codes, scales).double()
+    rx, rw, rb, mx, mw, mb = plain_norm_grad(dy, n, rstd, w)
+    dx, dw, db = A.layer_norm_keep_grad(dy, codes, scales, rstd, w)
+    within(dx, rx, mx + (U[dtype] + E) * rx.abs() + TINY[dtype], "dx")
+    c = chain(rows, hidden)
+    within(dw, rw, (c + 4) * E * mw + E * rw.abs(), "dweight")
+    within(db, rb, c * E * mb + E * rb.abs(), "dbias")
+
+
+def test_outputs_over_their_own_inputs_are_refused(gpu):
+    """Reading back over the codes or the scales, packing over the rows, and a
+    gradient over the tokens or the workspace."""
+    raw = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    codes, scales = raw[:256].view(torch.int8).view(8, 32), raw[256:264].view(8, 1)
+    for at in (0, 192, 252):
+        with pytest.raises(A.AdasumError, match="overlaps"):
+            A.checkpoint_unpack(codes, scales, out=raw[at:at + 1024].view(F32).view(8, 32))
+    x = raw[1024:2048].view(F32).view(8, 32)
+    with pytest.raises(A.AdasumError, match="overlaps"):
+        A.checkpoint_pack(x, codes=raw[1800:2056].view(torch.int8).view(8, 32))
+    with pytest.raises(A.AdasumError, match="overlaps"):
+        A.checkpoint_pack(x, scales=raw[1024:1032].view(8, 1))
+    tok = raw[2048:2112].view(torch.int64)
+    with pytest.raises(A.AdasumError, match="overlaps"):
+        A.embedding_grad(x, tok, 2, out=raw[2096:2352].view(F32))
+    need = _native.lib().adasum_layer_norm_grad_workspace_bytes(8, 32, 0)
+    stat, w = torch.ones(8, device="cuda"), torch.ones(32, device="cuda")
+    dw = torch.zeros(need, dtype=torch.uint8, device="cuda").view(F32)
+    with pytest.raises(A.AdasumError, match="overlaps"):
+        A.layer_norm_grad(x, x, stat, stat, w, dweight=dw[:32], workspace=dw)
+
+
 def test_linear_grad_of_codes_of_another_type(gpu):
     """fp16 products need fp16 values of x: codes packed from fp32 that are
     not show as infinities or NaN where they are too large, and cost half of
