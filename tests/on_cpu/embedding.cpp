@@ -11,29 +11,16 @@ thread_local int32_t counts[16 * 512];  // the grouping kernel's dynamic LDS
 }  // namespace adasum
 
 #include "embedding.inc"
+#include "values.h"
 
 using namespace adasum;
-
-static double value(const void* p, int dtype, int64_t i) {
-  if (dtype == 0) return static_cast<const float*>(p)[i];
-  if (dtype == 1) return (double)(float)static_cast<const _Float16*>(p)[i];
-  return (double)(float)static_cast<const __bf16*>(p)[i];
-}
-static void put(void* p, int dtype, int64_t i, float v) {
-  if (dtype == 0)
-    static_cast<float*>(p)[i] = v;
-  else if (dtype == 1)
-    static_cast<_Float16*>(p)[i] = (_Float16)v;
-  else
-    static_cast<__bf16*>(p)[i] = (__bf16)v;
-}
 
 int main(int, char** arg) {
   std::setvbuf(stdout, nullptr, _IONBF, 0);
   const int64_t n = std::atoll(arg[1]), vocab = std::atoll(arg[2]);
   const int hidden = std::atoi(arg[3]), kind = std::atoi(arg[4]), dtype = std::atoi(arg[5]), out = std::atoi(arg[6]);
   const int token_bytes = std::atoi(arg[7]), accumulate = std::atoi(arg[8]);
-  const size_t b = dtype == 0 ? 4 : 2, g = out == 0 ? 4 : 2;
+  const size_t b = size_of(dtype), g = size_of(out);
   std::srand(1);
   auto uniform = [] { return (std::rand() + 0.5) / (RAND_MAX + 1.0); };
 
@@ -58,9 +45,9 @@ int main(int, char** arg) {
     }
   }
   char* dy = on_cpu::guarded(n * hidden * b);
-  for (int64_t i = 0; i < n * hidden; ++i) put(dy, dtype, i, (float)(std::rand() % 129 - 64) / 64);
+  for (int64_t i = 0; i < n * hidden; ++i) put(dy, dtype, i, (std::rand() % 129 - 64) / 64.);
   char* grad = on_cpu::guarded(vocab * hidden * g);
-  for (int64_t i = 0; i < vocab * hidden; ++i) put(grad, out, i, accumulate ? (float)(i % 5) : 7777.f);
+  for (int64_t i = 0; i < vocab * hidden; ++i) put(grad, out, i, accumulate ? i % 5 : 7777.);
   const EmbeddingGradLayout l = embedding_grad_layout(n, hidden, dtype);
   char* ws = on_cpu::guarded(l.total);
   for (size_t i = 0; i < l.total; ++i) ws[i] = (char)(0x91 + i % 111);
@@ -90,7 +77,7 @@ int main(int, char** arg) {
   std::vector<double> sum(vocab * hidden, 0.0);
   for (int64_t r : rows)
     for (int c = 0; c < hidden; ++c) sum[token[r] * hidden + c] += value(dy, dtype, r * hidden + c);
-  const double half = out == 0 ? 0.0 : out == 1 ? std::exp2(-11) : std::exp2(-8);
+  const double half = out == 0 ? 0.0 : half_step(out);
   for (int64_t i = 0; i < vocab * hidden; ++i) {
     const double want = 0.5 * sum[i] + (accumulate ? (double)(i % 5) : 0.0);
     if (!(std::abs(value(grad, out, i) - want) <= std::abs(want) * half)) on_cpu::stop("a wrong sum");

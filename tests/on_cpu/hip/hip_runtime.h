@@ -4,7 +4,8 @@
 // barrier of the workgroup, or an operation of the wave (ballot, lane
 // exchange).  Waves are taken in random order, LDS starts as garbage, and a
 // meeting that not all lanes of a wave (or of a workgroup) come to ends the
-// program.  Every shared array is thread_local here, and nothing else of the
+// program, unless it allows a wave's lanes to divide: then those furthest back
+// in the code go on first.  Every shared array is thread_local here, and nothing else of the
 // program may be: that is how a new workgroup finds them to overwrite.
 #pragma once
 
@@ -54,12 +55,14 @@ struct Lane {
   void* sp;
   State state;
   uint64_t in, from, out;
+  const void* site;  // where in the code it waits
 };
 inline std::vector<Lane> lanes;
 inline std::vector<char*> stacks;
 inline unsigned current;
 inline void* scheduler;
 inline const std::function<void()>* body;
+inline bool may_divide = false;
 constexpr size_t kStack = 1 << 16;
 
 // Saves what a call must keep, and goes on with the other stack.
@@ -86,8 +89,9 @@ on_cpu_switch:
   ret
 )");
 
-inline void wait(State s) {
+__attribute__((noinline)) inline void wait(State s) {
   lanes[current].state = s;
+  lanes[current].site = __builtin_return_address(0);
   on_cpu_switch(&lanes[current].sp, scheduler);
 }
 inline void lane_main() {
@@ -100,7 +104,7 @@ inline void start(unsigned i) {
   *--top = nullptr;  // the return address of lane_main; rsp is then as after a call
   *--top = reinterpret_cast<void*>(&lane_main);
   for (int r = 0; r < 6; ++r) *--top = nullptr;
-  lanes[i] = Lane{top, kRun, 0, 0, 0};
+  lanes[i] = Lane{top, kRun, 0, 0, 0, nullptr};
 }
 
 // Every shared array of the program overwritten.
@@ -118,34 +122,44 @@ inline void spoil_lds() {
 }
 
 inline void run_wave(unsigned w) {
-  unsigned live = 0, meet[kDone + 1] = {};
-  for (unsigned i = w * 64; i < w * 64 + 64; ++i) {
-    if (lanes[i].state == kRun) {
-      current = i;
-      threadIdx.x = i;
-      on_cpu_switch(&scheduler, lanes[i].sp);
+  unsigned meet[kDone + 1] = {};
+  Lane* const wave = &lanes[w * 64];
+  for (unsigned l = 0; l < 64; ++l) {
+    if (wave[l].state == kRun) {
+      current = w * 64 + l;
+      threadIdx.x = current;
+      on_cpu_switch(&scheduler, wave[l].sp);
     }
-    ++meet[lanes[i].state];
-    live += lanes[i].state != kDone;
+    ++meet[wave[l].state];
   }
   const unsigned in_wave = meet[kBallot] + meet[kExchange] + meet[kOrder];
   if (in_wave == 0) return;  // all at a barrier or done
-  if (meet[kBarrier]) stop("a wave is divided between a barrier and an operation of its own");
-  if (std::max({meet[kBallot], meet[kExchange], meet[kOrder]}) != in_wave) stop("a wave meets at two operations");
+  const void* site = nullptr;
+  for (unsigned l = 0; l < 64; ++l)
+    if (wave[l].state != kBarrier && wave[l].state != kDone &&
+        (site == nullptr || std::less<const void*>()(wave[l].site, site)))
+      site = wave[l].site;
+  bool meets[64];
+  unsigned together = 0;
+  for (unsigned l = 0; l < 64; ++l) {
+    meets[l] = wave[l].state != kBarrier && wave[l].state != kDone && wave[l].site == site;
+    together += meets[l];
+  }
+  if (!may_divide && meet[kBarrier]) stop("a wave is divided between a barrier and an operation of its own");
+  if (!may_divide && together != in_wave) stop("a wave meets at two operations");
   uint64_t mask = 0;
   for (unsigned l = 0; l < 64; ++l)
-    if (lanes[w * 64 + l].state == kBallot && lanes[w * 64 + l].in) mask |= uint64_t(1) << l;
+    if (meets[l] && wave[l].state == kBallot && wave[l].in) mask |= uint64_t(1) << l;
   for (unsigned l = 0; l < 64; ++l) {
-    Lane& x = lanes[w * 64 + l];
-    if (x.state == kBallot) x.out = mask;
-    if (x.state == kExchange) {
-      const Lane& y = lanes[w * 64 + x.from];
-      if (y.state != kExchange) stop("a value of a lane that is not there");
-      x.out = y.in;
+    if (!meets[l]) continue;
+    if (wave[l].state == kBallot) wave[l].out = mask;
+    if (wave[l].state == kExchange) {
+      if (!meets[wave[l].from]) stop("a value of a lane that is not there");
+      wave[l].out = wave[wave[l].from].in;
     }
   }
   for (unsigned l = 0; l < 64; ++l)
-    if (lanes[w * 64 + l].state != kDone) lanes[w * 64 + l].state = kRun;
+    if (meets[l]) wave[l].state = kRun;
 }
 
 inline void run_workgroup(unsigned threads) {
@@ -200,7 +214,7 @@ inline char* guarded(size_t bytes) {
   return p + page + whole - bytes;
 }
 
-inline uint32_t exchange(uint32_t v, unsigned lane) {
+__forceinline__ uint32_t exchange(uint32_t v, unsigned lane) {
   Lane& l = lanes[current];
   l.in = v;
   l.from = lane;
@@ -209,17 +223,36 @@ inline uint32_t exchange(uint32_t v, unsigned lane) {
 }
 inline unsigned lane_id() { return current & 63; }
 
+// f(from): what the lane makes of the wave's values of v, from(l) being lane
+// l's.  No lane goes on before all have read.
+template <typename V, typename F>
+__forceinline__ auto together(const V& v, F f) {
+  Lane& l = lanes[current];
+  l.in = reinterpret_cast<uint64_t>(&v);
+  const unsigned wave = current & ~63u;
+  wait(kOrder);
+  auto out = f([wave](unsigned i) -> const V& {
+    if (lanes[wave + i].state == kDone) stop("a value of a lane that is not there");
+    return *reinterpret_cast<const V*>(lanes[wave + i].in);
+  });
+  wait(kOrder);
+  return out;
+}
+
 }  // namespace on_cpu
 
-inline void __syncthreads() { on_cpu::wait(on_cpu::kBarrier); }
-inline uint64_t __ballot(int p) {
+__forceinline__ void __syncthreads() { on_cpu::wait(on_cpu::kBarrier); }
+__forceinline__ uint64_t __ballot(int p) {
   on_cpu::lanes[on_cpu::current].in = p != 0;
   on_cpu::wait(on_cpu::kBallot);
   return on_cpu::lanes[on_cpu::current].out;
 }
-inline int __shfl_up(int v, unsigned by) {
+__forceinline__ int __shfl_up(int v, unsigned by) {
   const unsigned l = on_cpu::lane_id();
   return (int)on_cpu::exchange((uint32_t)v, l >= by ? l - by : l);
+}
+__forceinline__ float __shfl_xor(float v, unsigned by) {
+  return __builtin_bit_cast(float, on_cpu::exchange(__builtin_bit_cast(uint32_t, v), on_cpu::lane_id() ^ by));
 }
 inline int __popcll(uint64_t x) { return __builtin_popcountll(x); }
 inline int32_t atomicAdd(int32_t* p, int32_t v) {
@@ -230,7 +263,7 @@ inline int32_t atomicAdd(int32_t* p, int32_t v) {
 inline int on_cpu_mbcnt(uint64_t mask, int add) {
   return add + __builtin_popcountll(mask & ((uint64_t(1) << on_cpu::lane_id()) - 1));
 }
-inline int on_cpu_dpp(int v, int ctrl) {
+__forceinline__ int on_cpu_dpp(int v, int ctrl) {
   const unsigned l = on_cpu::lane_id();
   unsigned from = 0;
   if (ctrl < 0x100)  // of each four lanes
@@ -251,3 +284,50 @@ inline int on_cpu_dpp(int v, int ctrl) {
 #define __builtin_amdgcn_wave_barrier() on_cpu::wait(on_cpu::kOrder)
 #define __builtin_amdgcn_update_dpp(old, v, ctrl, rows, banks, bound) on_cpu_dpp(v, ctrl)
 #define __builtin_amdgcn_fmed3f(a, b, c) std::min(std::max(a, b), c)
+#define __builtin_amdgcn_rsqf(x) (1.f / std::sqrt(x))
+#define __builtin_amdgcn_sched_barrier(mask) ((void)0)
+
+inline uint32_t on_cpu_perm(uint32_t hi, uint32_t lo, uint32_t select) {
+  const uint64_t both = (uint64_t)hi << 32 | lo;
+  uint32_t r = 0;
+  for (int i = 0; i < 4; ++i) r |= (uint32_t)(both >> (8 * ((select >> (8 * i)) & 7)) & 0xff) << (8 * i);
+  return r;
+}
+#define __builtin_amdgcn_perm(hi, lo, select) on_cpu_perm(hi, lo, select)
+
+// Lane i of 16 names four values of row i / 4 and gets value i of the four
+// rows: the four that lane 4 r + i / 4 names hold row r's.
+template <typename P>
+__forceinline__ auto on_cpu_read_turned(P p) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  const v4s mine = *p;
+  return on_cpu::together(mine, [](auto from) {
+    const unsigned l = on_cpu::lane_id(), i = l & 15;
+    v4s r;
+    for (unsigned k = 0; k < 4; ++k) r[k] = from((l & ~15u) + 4 * k + i / 4)[i & 3];
+    return r;
+  });
+}
+#define __builtin_amdgcn_ds_read_tr16_b64_v4i16(p) on_cpu_read_turned(p)
+
+// A lane of a 16 x 16 x 32 product holds terms 8 (l / 16) .. of row or column
+// l % 16, and of the sums rows 4 (l / 16) .. of column l % 16.
+template <typename V, typename C>
+__forceinline__ C on_cpu_multiply(V a, V b, C c) {
+  struct Both {
+    V a, b;
+  } mine{a, b};
+  return on_cpu::together(mine, [&](auto from) {
+    const unsigned l = on_cpu::lane_id();
+    C r = c;
+    for (unsigned q = 0; q < 4; ++q) {
+      float sum = 0.f;
+      for (unsigned k = 0; k < 32; ++k)
+        sum += (float)from(k / 8 * 16 + l / 16 * 4 + q).a[k % 8] * (float)from(k / 8 * 16 + l % 16).b[k % 8];
+      r[q] += sum;
+    }
+    return r;
+  });
+}
+#define __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, x, y, z) on_cpu_multiply(a, b, c)
+#define __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, x, y, z) on_cpu_multiply(a, b, c)

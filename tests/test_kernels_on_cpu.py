@@ -80,3 +80,21 @@ F32, F16, BF16 = range(3)
 def test_embedding_grad(program, n, vocab, hidden, kind, dtype, grad, token_bytes, accumulate):
     """The grouped list is right at every position and the sums are exact."""
     run(program("embedding"), n, vocab, hidden, kind, dtype, grad, token_bytes, accumulate)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,hidden", [(1, 1), (37, 7), (70, 100), (33, 250), (9, 513), (6, 1001), (5, 2050),
+                                         (3, 4097), (2, 16384), (2, 16383)])
+def test_layer_norm(program, rows, hidden, dtype):
+    """Forward and backward, from x and from kept rows, rows with gaps."""
+    for kept in (0, 1):
+        run(program("layer_norm"), rows, hidden, dtype, kept, (rows + kept) % 2)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,out,width", [(1, 1, 1), (33, 7, 15), (31, 8, 16), (70, 130, 5), (65, 3, 300),
+                                            (100, 140, 270), (300, 40, 33), (129, 259, 257)])
+def test_linear_grad(program, rows, out, width, dtype):
+    """Exact sums of narrow and ragged operands, rows with gaps."""
+    for grad in {F32, dtype}:
+        run(program("linear_grad"), rows, out, width, dtype, grad, rows % 2)
