@@ -224,7 +224,7 @@ std::vector<std::pair<hipEvent_t, hipEvent_t>> g_ev_pool;  // guarded by g_mu
 
 // Records the start event of a launch; returns the record index or -1.
 int prof_start(int kind, double bytes, hipStream_t st) {
-  if (!g_prof_on) return -1;
+  if (!g_prof_on || capturing(st)) return -1;  // an event of a graph has no time to read
   std::pair<hipEvent_t, hipEvent_t> ev{nullptr, nullptr};
   if (!g_ev_pool.empty()) {
     ev = g_ev_pool.back();

@@ -1345,3 +1345,32 @@ def test_linear_grad_of_codes_of_another_type(gpu):
         bw, _ = linear_bound(dy.to(dtype), back, rows, dtype)
         want = dy.to(dtype).double().t() @ back
         within(dw, want, bw + 2 * E * want.abs(), f"dweight {dtype}")
+
+
+def test_timed_while_captured(gpu):
+    """With launch timing on, captured calls are left out of it and eager ones
+    counted, of the layer operators and of the combine."""
+    run = all_calls(270, BF16)
+    grads = [randn(280 + k, 5000) for k in range(3)]
+    out = torch.empty(5000, device="cuda")
+    off = [0, 2000, 5000]
+    want = A.combine(grads, off).clone()
+    run()
+    torch.cuda.synchronize()
+    _native.profile_begin()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = run()
+        A.combine(grads, off, out=out)
+    eager = run()
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+    times = _native.profile_end()
+    # embedding and its gradient; two norms and two gradients; pack and back
+    assert {k: v["launches"] for k, v in times.items()} == {"embedding": 2, "norm": 4, "pack": 2, "linear": 1}
+    assert all(v["milliseconds"] > 0 for v in times.values())
+    assert same(captured, eager) and torch.equal(out, want)
+    _native.profile_begin()
+    A.combine(grads, off, out=out)
+    assert sum(v["launches"] for v in _native.profile_end().values()) > 0
