@@ -272,6 +272,9 @@ ADASUM_API int adasum_embedding_grad(const void* dy, int64_t n, int64_t hidden, 
 /*
  * adasum_layer_norm - y = (x - mean) * rstd * weight + bias for every row,
  * with mean the row's mean and rstd = 1 / sqrt(variance + eps).
+ * Where a row's sum passes fp32's range, its outputs are NaN; where only its
+ * squared deviations do (deviations from some 10^17 on), rstd is 0 and y the
+ * bias.
  *
  *   x, y         rows x hidden elements of dtype, hidden <= 16384.
  *   weight, bias hidden elements of param_dtype each; NULL: 1 and 0.

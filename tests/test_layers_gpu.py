@@ -1374,3 +1374,18 @@ def test_timed_while_captured(gpu):
     _native.profile_begin()
     A.combine(grads, off, out=out)
     assert sum(v["launches"] for v in _native.profile_end().values()) > 0
+
+
+def test_layer_norm_out_of_range(gpu):
+    """Rows whose sum passes fp32's range are NaN; where only the squares do,
+    rstd is 0 and y the bias.  The rows beside them do not notice."""
+    for dtype in (F32, BF16):
+        x, w, b = randn(290, 4, 600, dtype=dtype), randn(291, 600), randn(292, 600)
+        want = A.layer_norm(x, w, b)
+        big = x.clone()
+        big[1] *= 1e25
+        big[2] = 1e38
+        y, mean, rstd = A.layer_norm(big, w, b)
+        assert torch.equal(y[[0, 3]], want[0][[0, 3]])
+        assert float(rstd[1]) == 0 and torch.equal(y[1], b.to(dtype))
+        assert bool(y[2].isnan().all()) and bool(rstd[2].isnan())
