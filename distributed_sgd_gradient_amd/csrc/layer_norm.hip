@@ -15,8 +15,8 @@
 //
 // Measured, bf16 (fp32 parameters): forward of 65536 x 1024 with kept rows 79
 // us (4.3 TB/s), 524288 x 128 54 us (5.0), 8192 x 16384 115 us (4.7); backward
-// of 65536 x 1024 from x 75 + 5 us (5.1), 524288 x 128 81 us (5.0), 8192 x
-// 16384 162 us (5.0).
+// of 65536 x 1024 from x 75 + 5 us (5.1), from kept rows 63 + 5 us (4.9),
+// 524288 x 128 81 us (5.0), 8192 x 16384 162 us (5.0).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
