@@ -21,7 +21,8 @@ constexpr int64_t kMaxDim = int64_t(1) << 31;  // rows, tokens, vocabulary and w
 constexpr int64_t kMaxEmbeddingHidden = int64_t(1) << 23;  // a launch has 65536 workgroups along a row at most
 // Rows that one fp32 sum of the linear gradient takes at most.  A split more of
 // a dweight too large to be split otherwise costs the writing and reading of
-// its partial sums, 8 bytes beside the 131072 operations of each.
+// its partial sums, 8 bytes beside the 131072 operations of each: 262144,
+// 30522 x 1024 bf16 15840 us in four splits, 15890 in one.
 constexpr int64_t kMaxLinearRows = 65536;
 // Row stride of the linear gradient's dy: a row's offset is the product of two
 // 32-bit numbers, the row and the stride in bytes.

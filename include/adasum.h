@@ -370,12 +370,13 @@ ADASUM_API int adasum_linear_grad(const void* dy, int64_t rows, int64_t out_feat
  * Kernel timing, for benchmarks.  Between adasum_profile_begin() and
  * adasum_profile_end(), every kernel launch that any combine call of this
  * process enqueues (and the launches of every layer operator's call, as one)
- * is bracketed by a pair of HIP events recorded on that
- * call's stream; launches captured into a graph are not recorded.  adasum_profile_end() waits for those events, disables the
- * recording, and writes one row per kernel kind: the launch count, the summed
- * launch durations and the summed algorithmic bytes (every operand read
- * once, every result written once).  Returns the number of rows written (at
- * most max_rows; rows may be NULL when max_rows is 0) or a negative code.
+ * is bracketed by a pair of HIP events recorded on that call's stream;
+ * launches captured into a graph are not recorded.  adasum_profile_end() waits
+ * for those events, disables the recording, and writes one row per kernel kind:
+ * the launch count, the summed launch durations and the summed algorithmic
+ * bytes (every operand read once, every result written once).  Returns the
+ * number of rows written (at most max_rows; rows may be NULL when max_rows is
+ * 0) or a negative code.
  */
 typedef struct {
   char kernel[32];     /* "gram", "tree", "exact", "wsum" (a small combine's
