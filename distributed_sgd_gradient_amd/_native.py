@@ -45,6 +45,19 @@ SIGNATURES = {
     "adasum_linear_grad_workspace_bytes": (_I64, [_I64, _I64, _I64, _INT]),
     "adasum_linear_grad": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _VP, _I64, _VP, _VP, _INT, _INT, _VP,
                                   ctypes.c_size_t, _VP]),
+    "adasum_rms": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _I64, _INT, _VP, _INT, _F64, _VP, _I64, _VP, _I64, _VP,
+                          _VP, _VP, _VP]),
+    "adasum_rms_grad_workspace_bytes": (_I64, [_I64, _I64, _INT]),
+    "adasum_rms_grad": (_INT, [_VP, _I64, _I64, _I64, _INT, _VP, _I64, _INT, _VP, _I64, _VP, _VP, _INT, _VP, _I64,
+                               _VP, _INT, _INT, _VP, ctypes.c_size_t, _VP]),
+    "adasum_relative_bias": (_INT, [_VP, _I64, _I64, _I64, _INT, _I64, _INT, _I64, _I64, _I64, _I64, _VP, _I64, _VP,
+                                    _I64, _INT, _VP]),
+    "adasum_relative_bias_grad_workspace_bytes": (_I64, [_I64, _I64, _I64, _I64, _INT]),
+    "adasum_relative_bias_grad": (_INT, [_VP, _I64, _I64, _I64, _I64, _I64, _INT, _I64, _I64, _I64, _INT, _VP, _INT,
+                                         _INT, _VP, ctypes.c_size_t, _VP]),
+    "adasum_orthogonalize_workspace_bytes": (_I64, [_I64, _I64, _I64, _INT]),
+    "adasum_orthogonalize": (_INT, [_VP, _I64, _I64, _I64, _I64, _INT, _INT, _VP, _F64, _F64, _VP, _I64, _INT, _VP,
+                                    ctypes.c_size_t, _VP]),
     "adasum_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "adasum_last_error": (ctypes.c_char_p, []),
     "adasum_version": (ctypes.c_int, []),

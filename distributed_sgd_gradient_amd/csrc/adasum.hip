@@ -210,7 +210,8 @@ std::map<std::pair<int, void*>, OwnedWorkspace> g_ws;  // (device, stream) -> bu
 
 // ---------------------------------------------------------------- launch timing
 
-const char* const kKindNames[kNumKinds] = {"gram", "tree", "wsum", "sum", "exact", "embedding", "norm", "pack", "linear"};
+const char* const kKindNames[kNumKinds] = {"gram", "tree", "wsum", "sum", "exact", "embedding", "norm", "pack", "linear",
+                                         "bias", "orthogonal"};
 
 struct ProfRecord {
   int kind;

@@ -81,6 +81,133 @@ struct NormGradArgs {
 int64_t norm_grad_parts(int64_t rows, int hidden);
 hipError_t launch_norm_grad(int dtype, const NormGradArgs& a, hipStream_t st);
 
+// ---------------------------------------------------------------- root-mean-square norm
+
+// The residual stream (residual, h, dh, dx) is of x's type or fp32.
+struct RmsArgs {
+  const void* x;
+  const void* residual;  // NULL: h = x, and R is x's type
+  int64_t rows, x_stride, residual_stride, y_stride, h_stride;
+  int hidden;
+  const void* weight;  // NULL: 1
+  int param_dtype;
+  float eps;
+  void* y;  // may be NULL with codes
+  void* h;  // may be NULL
+  float* rstd;
+  int8_t* codes;  // NULL: y is not given in 8 bits
+  uint8_t* scales;
+};
+hipError_t launch_rms(int dtype, int stream_dtype, const RmsArgs& a, hipStream_t st);
+
+struct RmsGradArgs {
+  const void* dy;
+  const void* h;
+  const void* dh;  // NULL: 0
+  int64_t rows, dy_stride, h_stride, dh_stride, dx_stride;
+  int hidden;
+  const float* rstd;
+  const void* weight;  // NULL: 1
+  int param_dtype;
+  void* dx;
+  void* dweight;  // NULL: not wanted
+  int grad_dtype;
+  int accumulate;
+  float* partials;  // rms_grad_parts(...) x hidden
+};
+int64_t rms_grad_parts(int64_t rows, int hidden);
+hipError_t launch_rms_grad(int dtype, int stream_dtype, const RmsGradArgs& a, hipStream_t st);
+
+// ---------------------------------------------------------------- relative bias
+
+constexpr int kMaxBuckets = 256;
+constexpr int64_t kMaxReach = int64_t(1) << 30;
+
+// Where the buckets of one side begin: border[k] <= distance < border[k + 1],
+// and no end behind the last.
+struct BiasBuckets {
+  int both;  // the keys behind the query have buckets of their own, side ..
+  int side;  // buckets of a side
+  uint32_t border[kMaxBuckets];
+};
+BiasBuckets bias_buckets(int buckets, int64_t reach, bool both);
+
+struct BiasArgs {
+  const void* table;  // buckets x heads
+  int64_t table_stride;
+  int table_dtype;
+  BiasBuckets buckets;
+  int64_t batch, heads, queries, keys, offset;
+  const void* scores;  // NULL: the bias alone
+  int64_t scores_stride, out_stride;
+  void* out;
+};
+struct BiasLayout {
+  int64_t row_tiles, col_tiles, part_batch, blocks;
+};
+BiasLayout bias_layout(int64_t batch, int64_t heads, int64_t queries, int64_t keys);
+hipError_t launch_bias(int dtype, const BiasArgs& a, hipStream_t st);
+
+struct BiasGradArgs {
+  const void* dscores;
+  int64_t stride;
+  BiasBuckets buckets;
+  int buckets_total;
+  int64_t batch, heads, queries, keys, offset;
+  void* dtable;
+  int grad_dtype;
+  int accumulate;
+  float* partials;
+};
+// Workgroups of the gradient: tiles of diagonals, heads, and splits of the rows.
+struct BiasGradLayout {
+  int lanes;  // that share a row
+  int64_t tiles, splits, blocks;
+  size_t bytes;
+};
+BiasGradLayout bias_grad_layout(int64_t batch, int64_t heads, int64_t queries, int64_t keys, int dtype);
+hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st);
+
+// ---------------------------------------------------------------- orthogonal updates
+
+constexpr int kOrthoTogether = 32;  // matrices of one launch at most
+constexpr int kOrthoSteps = 16;
+constexpr int64_t kMaxOrthoSide = int64_t(1) << 15;
+
+// Where a matrix's pieces lie in its part of the workspace (byte offsets), n x
+// m its sides, the shorter first, padded to whole tiles; [0] high parts, [1]
+// low parts.
+struct OrthoLayout {
+  int64_t n, m;
+  int parts, tile, together;  // together: matrices of one launch
+  size_t x[2], xt[2][2], a[2], b[2], rest, sums;  // xt: of even and odd steps
+  size_t per_matrix, total;
+};
+OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtype);
+
+struct OrthoArgs {
+  const void* x[kOrthoTogether];
+  void* out[kOrthoTogether];
+  int64_t rows, cols, x_stride, out_stride;
+  int out_dtype, steps;
+  double eps;
+  float scale;
+  float coefficients[3 * kOrthoSteps];
+  char* ws;
+};
+struct OrthoStep {
+  float a, b, c;
+  int from;  // the transpose to read; the other one is written
+  int last;
+};
+struct OrthoCall {
+  OrthoArgs args;  // without x and out
+  int64_t count;
+  const void* const* x;
+  void* const* out;
+};
+hipError_t launch_ortho(int dtype, const OrthoCall& call, hipStream_t st);
+
 // ---------------------------------------------------------------- 8-bit activations
 
 struct PackArgs {

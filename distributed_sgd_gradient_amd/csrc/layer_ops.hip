@@ -7,12 +7,15 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <exception>
 #include <mutex>
 #include <new>
+#include <string>
+#include <vector>
 
 #include "../../include/adasum.h"
 #include "library.h"
@@ -25,6 +28,7 @@ size_t size_of(int d) { return d == ADASUM_F32 ? 4 : 2; }
 
 constexpr int64_t kMaxElements = int64_t(1) << 40;
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
+constexpr int64_t kMaxOrthoCount = int64_t(1) << 16;
 
 // One buffer argument: where it lies and what a call does with it.
 struct Buffer {
@@ -421,6 +425,372 @@ int linear_grad(const void* dy, int64_t rows, int64_t out, int64_t dy_stride, in
   return launch(kLinear, "linear gradient", bytes, st, [&] { return launch_linear_grad(dtype, a, st); });
 }
 
+int check_params(int64_t hidden, int param_dtype, double eps) {
+  if (hidden > kMaxNormHidden) return fail(ADASUM_EINVAL, "root-mean-square norm: hidden must be at most 16384");
+  if (!known_dtype(param_dtype)) return fail(ADASUM_EINVAL, "unknown param_dtype");
+  if (!std::isfinite((float)eps) || (float)eps < FLT_MIN)
+    return fail(ADASUM_EINVAL, "eps must be a positive normal fp32 number");
+  return ADASUM_OK;
+}
+
+// The residual stream is of x's type or fp32.
+int check_stream(int dtype, int stream_dtype) {
+  if (!known_dtype(dtype)) return fail(ADASUM_EINVAL, "unknown dtype");
+  if (stream_dtype != dtype && stream_dtype != ADASUM_F32)
+    return fail(ADASUM_EINVAL, "stream_dtype must be dtype or fp32");
+  return ADASUM_OK;
+}
+
+int rms(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, int dtype, const void* residual,
+        int64_t residual_stride, int stream_dtype, const void* weight, int param_dtype, double eps, void* y,
+        int64_t y_stride, void* h, int64_t h_stride, float* rstd, int8_t* codes, uint8_t* scales, void* stream) {
+  size_t x_bytes = 0, residual_bytes = 0, y_bytes = 0, h_bytes = 0;
+  RETURN_IF(check_stream(dtype, stream_dtype));
+  RETURN_IF(check_matrix(rows, hidden, x_stride, dtype, "x", &x_bytes));
+  if (residual) RETURN_IF(check_matrix(rows, hidden, residual_stride, stream_dtype, "residual", &residual_bytes));
+  if (y || !codes) RETURN_IF(check_matrix(rows, hidden, y_stride, dtype, "y", &y_bytes));
+  if (h) RETURN_IF(check_matrix(rows, hidden, h_stride, stream_dtype, "h", &h_bytes));
+  RETURN_IF(check_params(hidden, param_dtype, eps));
+  if ((codes == nullptr) != (scales == nullptr)) return fail(ADASUM_EINVAL, "codes and scales belong together");
+  if (rows == 0) return ADASUM_OK;
+  if (h && !residual) return fail(ADASUM_EINVAL, "without a residual there is no h: it is x");
+  if (!residual && stream_dtype != dtype) return fail(ADASUM_EINVAL, "without a residual stream_dtype must be dtype");
+  if (h && h == residual && h_stride == residual_stride) residual_bytes = 0;  // in place
+  const Buffer b[] = {{x, x_bytes, size_of(dtype), "x", false},
+                      {residual, residual_bytes, size_of(stream_dtype), "residual", false},
+                      {weight, weight ? (size_t)hidden * size_of(param_dtype) : 0, size_of(param_dtype), "weight", false},
+                      {y, y_bytes, size_of(dtype), "y", true},
+                      {h, h_bytes, size_of(stream_dtype), "h", true},
+                      {rstd, (size_t)rows * 4, 4, "rstd", true},
+                      {codes, codes ? (size_t)(rows * hidden) : 0, 1, "codes", true},
+                      {scales, codes ? (size_t)(rows * ceil_div(hidden, kScaleBlock)) : 0, 1, "scales", true}};
+  RETURN_IF(check_buffers(b));
+  RmsArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.rows = rows;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.y_stride = y_stride;
+  a.h_stride = h_stride;
+  a.hidden = (int)hidden;
+  a.weight = weight;
+  a.param_dtype = param_dtype;
+  a.eps = (float)eps;
+  a.y = y;
+  a.h = h;
+  a.rstd = rstd;
+  a.codes = codes;
+  a.scales = scales;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const double wide = (residual ? 1 : 0) * size_of(stream_dtype) + (h ? 1 : 0) * size_of(stream_dtype);
+  const double bytes =
+      (double)rows * ((double)hidden * ((y ? 2 : 1) * size_of(dtype) + wide + (codes ? 33.0 / 32 : 0.0)) + 4);
+  return launch(kNorm, "root-mean-square norm", bytes, st, [&] { return launch_rms(dtype, stream_dtype, a, st); });
+}
+
+size_t rms_grad_workspace(int64_t rows, int64_t hidden) {
+  return rows == 0 ? 0 : (size_t)rms_grad_parts(rows, (int)hidden) * hidden * sizeof(float);
+}
+
+int64_t rms_grad_bytes(int64_t rows, int64_t hidden, int dtype) {
+  size_t bytes = 0;
+  RETURN_IF(check_matrix(rows, hidden, hidden, dtype, "dy", &bytes));
+  if (hidden > kMaxNormHidden) return fail(ADASUM_EINVAL, "root-mean-square norm: hidden must be at most 16384");
+  return (int64_t)rms_grad_workspace(rows, hidden);
+}
+
+int rms_grad(const void* dy, int64_t rows, int64_t hidden, int64_t dy_stride, int dtype, const void* h,
+             int64_t h_stride, int stream_dtype, const void* dh, int64_t dh_stride, const float* rstd,
+             const void* weight, int param_dtype, void* dx, int64_t dx_stride, void* dweight, int grad_dtype,
+             int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t dy_bytes = 0, h_bytes = 0, dh_bytes = 0, dx_bytes = 0;
+  RETURN_IF(check_stream(dtype, stream_dtype));
+  RETURN_IF(check_matrix(rows, hidden, dy_stride, dtype, "dy", &dy_bytes));
+  RETURN_IF(check_matrix(rows, hidden, h_stride, stream_dtype, "h", &h_bytes));
+  if (dh) RETURN_IF(check_matrix(rows, hidden, dh_stride, stream_dtype, "dh", &dh_bytes));
+  RETURN_IF(check_matrix(rows, hidden, dx_stride, stream_dtype, "dx", &dx_bytes));
+  RETURN_IF(check_params(hidden, param_dtype, 1.0));
+  if (!known_dtype(grad_dtype)) return fail(ADASUM_EINVAL, "unknown grad_dtype");
+  if (rows == 0 && (accumulate || !dweight)) return ADASUM_OK;
+  const size_t need = dweight ? rms_grad_workspace(rows, hidden) : 0;
+  RETURN_IF(check_workspace(workspace, workspace_bytes, need));
+  if (dh && dx == dh && dx_stride == dh_stride) dh_bytes = 0;  // in place
+  const Buffer b[] = {{dy, dy_bytes, size_of(dtype), "dy", false},
+                      {h, h_bytes, size_of(stream_dtype), "h", false},
+                      {dh, dh_bytes, size_of(stream_dtype), "dh", false},
+                      {rstd, (size_t)rows * 4, 4, "rstd", false},
+                      {weight, weight ? (size_t)hidden * size_of(param_dtype) : 0, size_of(param_dtype), "weight", false},
+                      {dx, dx_bytes, size_of(stream_dtype), "dx", true},
+                      {dweight, dweight ? (size_t)hidden * size_of(grad_dtype) : 0, size_of(grad_dtype), "dweight", true},
+                      {workspace, need, 16, "workspace", true}};
+  RETURN_IF(check_buffers(b));
+  RmsGradArgs a{};
+  a.dy = dy;
+  a.h = h;
+  a.dh = dh;
+  a.rows = rows;
+  a.dy_stride = dy_stride;
+  a.h_stride = h_stride;
+  a.dh_stride = dh_stride;
+  a.dx_stride = dx_stride;
+  a.hidden = (int)hidden;
+  a.rstd = rstd;
+  a.weight = weight;
+  a.param_dtype = param_dtype;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.grad_dtype = grad_dtype;
+  a.accumulate = accumulate != 0;
+  a.partials = dweight ? static_cast<float*>(workspace) : nullptr;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const double bytes =
+      (double)rows * ((double)hidden * (size_of(dtype) + (dh ? 3 : 2) * size_of(stream_dtype)) + 4);
+  return launch(kNorm, "root-mean-square norm gradient", bytes, st,
+                [&] { return launch_rms_grad(dtype, stream_dtype, a, st); });
+}
+
+int check_bias(int64_t heads, int64_t batch, int64_t queries, int64_t keys, int64_t offset, int64_t buckets,
+               int64_t max_distance, int bidirectional) {
+  if (heads < 1 || heads >= kMaxDim) return fail(ADASUM_EINVAL, "heads must be in [1, 2^31)");
+  if (batch < 0 || batch >= kMaxDim) return fail(ADASUM_EINVAL, "batch must be in [0, 2^31)");
+  if (queries < 0 || queries >= kMaxDim) return fail(ADASUM_EINVAL, "queries must be in [0, 2^31)");
+  if (keys < 1 || keys >= kMaxDim) return fail(ADASUM_EINVAL, "keys must be in [1, 2^31)");
+  if (batch * heads >= kMaxDim || batch * heads * queries >= kMaxDim)
+    return fail(ADASUM_EINVAL, "relative bias: the number of rows must be below 2^31");
+  if (offset <= -kMaxDim || offset >= kMaxDim) return fail(ADASUM_EINVAL, "offset must be within 2^31");
+  if (buckets < (bidirectional ? 4 : 2) || buckets > kMaxBuckets || (bidirectional && buckets % 2 != 0))
+    return fail(ADASUM_EINVAL, "buckets must be in [2, 256], in both directions even and at least 4");
+  const int64_t exact = (bidirectional ? buckets / 2 : buckets) / 2;
+  if (max_distance <= exact || max_distance > kMaxReach)
+    return fail(ADASUM_EINVAL, "max_distance must be above half the buckets of a side, and at most 2^30");
+  return ADASUM_OK;
+}
+
+// Workgroups of a launch: 256 lanes each, 2^32 lanes at most.
+constexpr int64_t kMaxBlocks = int64_t(1) << 24;
+
+int relative_bias(const void* table, int64_t buckets, int64_t heads, int64_t table_stride, int table_dtype,
+                  int64_t max_distance, int bidirectional, int64_t batch, int64_t queries, int64_t keys,
+                  int64_t offset, const void* scores, int64_t scores_stride, void* out, int64_t out_stride, int dtype,
+                  void* stream) {
+  size_t table_bytes = 0, scores_bytes = 0, out_bytes = 0;
+  RETURN_IF(check_bias(heads, batch, queries, keys, offset, buckets, max_distance, bidirectional));
+  RETURN_IF(check_matrix(buckets, heads, table_stride, table_dtype, "table", &table_bytes));
+  const int64_t rows = batch * heads * queries;
+  if (scores) RETURN_IF(check_matrix(rows, keys, scores_stride, dtype, "scores", &scores_bytes));
+  RETURN_IF(check_matrix(rows, keys, out_stride, dtype, "out", &out_bytes));
+  if (rows == 0) return ADASUM_OK;
+  if (bias_layout(batch, heads, queries, keys).blocks >= kMaxBlocks)
+    return fail(ADASUM_EINVAL, "relative bias: the scores are too large for one call");
+  if (out == scores && out_stride == scores_stride) scores_bytes = 0;  // in place
+  const Buffer b[] = {{table, table_bytes, size_of(table_dtype), "table", false},
+                      {scores, scores_bytes, size_of(dtype), "scores", false},
+                      {out, out_bytes, size_of(dtype), "out", true}};
+  RETURN_IF(check_buffers(b));
+  BiasArgs a{};
+  a.table = table;
+  a.table_stride = table_stride;
+  a.table_dtype = table_dtype;
+  a.buckets = bias_buckets((int)buckets, max_distance, bidirectional != 0);
+  a.batch = batch;
+  a.heads = heads;
+  a.queries = queries;
+  a.keys = keys;
+  a.offset = offset;
+  a.scores = scores;
+  a.scores_stride = scores_stride;
+  a.out_stride = out_stride;
+  a.out = out;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const double bytes = (double)rows * keys * size_of(dtype) * (scores ? 2 : 1);
+  return launch(kBias, "relative bias", bytes, st, [&] { return launch_bias(dtype, a, st); });
+}
+
+int check_bias_grad(int64_t batch, int64_t heads, int64_t queries, int64_t keys, int64_t stride, int dtype,
+                    size_t* bytes) {
+  const int64_t rows = batch * heads * queries;
+  RETURN_IF(check_matrix(rows, keys, stride, dtype, "dscores", bytes));
+  if (bias_grad_layout(rows == 0 ? 0 : batch, heads, std::max<int64_t>(queries, 1), keys, dtype).blocks >= kMaxBlocks ||
+      heads * kMaxBuckets >= kMaxBlocks)
+    return fail(ADASUM_EINVAL, "relative bias: the scores are too large for one call");
+  return ADASUM_OK;
+}
+
+int64_t relative_bias_grad_bytes(int64_t batch, int64_t heads, int64_t queries, int64_t keys, int dtype) {
+  size_t bytes = 0;
+  RETURN_IF(check_bias(heads, batch, queries, keys, 0, 4, 4, 1));
+  RETURN_IF(check_bias_grad(batch, heads, queries, keys, keys, dtype, &bytes));
+  return (int64_t)bias_grad_layout(bytes == 0 ? 0 : batch, heads, std::max<int64_t>(queries, 1), keys, dtype).bytes;
+}
+
+int relative_bias_grad(const void* dscores, int64_t batch, int64_t heads, int64_t queries, int64_t keys,
+                       int64_t stride, int dtype, int64_t offset, int64_t buckets, int64_t max_distance,
+                       int bidirectional, void* dtable, int grad_dtype, int accumulate, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  size_t in_bytes = 0, table_bytes = 0;
+  RETURN_IF(check_bias(heads, batch, queries, keys, offset, buckets, max_distance, bidirectional));
+  RETURN_IF(check_bias_grad(batch, heads, queries, keys, stride, dtype, &in_bytes));
+  RETURN_IF(check_matrix(buckets, heads, heads, grad_dtype, "dtable", &table_bytes));
+  if (in_bytes == 0) {  // no rows: a gradient of zeros
+    if (accumulate) return ADASUM_OK;
+    batch = 0;
+    queries = std::max<int64_t>(queries, 1);
+  }
+  const BiasGradLayout l = bias_grad_layout(batch, heads, queries, keys, dtype);
+  RETURN_IF(check_workspace(workspace, workspace_bytes, l.bytes));
+  const Buffer b[] = {{dscores, in_bytes, size_of(dtype), "dscores", false},
+                      {dtable, table_bytes, size_of(grad_dtype), "dtable", true},
+                      {workspace, l.bytes, 16, "workspace", true}};
+  RETURN_IF(check_buffers(b));
+  BiasGradArgs a{};
+  a.dscores = dscores;
+  a.stride = stride;
+  a.buckets = bias_buckets((int)buckets, max_distance, bidirectional != 0);
+  a.buckets_total = (int)buckets;
+  a.batch = batch;
+  a.heads = heads;
+  a.queries = queries;
+  a.keys = keys;
+  a.offset = offset;
+  a.dtable = dtable;
+  a.grad_dtype = grad_dtype;
+  a.accumulate = accumulate != 0;
+  a.partials = static_cast<float*>(workspace);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const double bytes = (double)batch * heads * queries * keys * size_of(dtype);
+  return launch(kBias, "relative bias gradient", bytes, st, [&] { return launch_bias_grad(dtype, a, st); });
+}
+
+// The buffers of a call with any number of them, as check_buffers.
+int check_many(const std::vector<Buffer>& given, const std::vector<int>& index) {
+  std::vector<size_t> order;
+  auto name = [&](size_t i) {
+    return std::string(given[i].name) + (index[i] < 0 ? "" : "[" + std::to_string(index[i]) + "]");
+  };
+  for (size_t i = 0; i < given.size(); ++i) {
+    const Buffer& x = given[i];
+    if (x.bytes == 0) continue;
+    if (x.p == nullptr) return einval("%s is NULL", name(i).c_str());
+    if (reinterpret_cast<uintptr_t>(x.p) % x.align != 0)
+      return einval("%s is not aligned to its elements", name(i).c_str());
+    order.push_back(i);
+  }
+  auto start = [&](size_t i) { return reinterpret_cast<uintptr_t>(given[i].p); };
+  std::sort(order.begin(), order.end(), [&](size_t i, size_t j) { return start(i) < start(j); });
+  uintptr_t end[2] = {0, 0};  // of what is read, of what is written, up to here
+  size_t by[2] = {0, 0};
+  for (size_t i : order) {
+    for (int w = 0; w < 2; ++w)
+      if ((w == 1 || given[i].written) && start(i) < end[w])
+        return einval("%s", (name(i) + " overlaps " + name(by[w])).c_str());
+    const int w = given[i].written ? 1 : 0;
+    if (start(i) + given[i].bytes > end[w]) {
+      end[w] = start(i) + given[i].bytes;
+      by[w] = i;
+    }
+  }
+  int device = 0;
+  const hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
+  uintptr_t lo = 0, last = 0;  // of the allocation that was asked for last
+  for (size_t i : order) {
+    if (start(i) >= lo && start(i) < last && given[i].bytes <= last - start(i)) continue;
+    lo = last = 0;
+    RETURN_IF(check_device_range(given[i].p, given[i].bytes, name(i).c_str(), device, &lo, &last));
+  }
+  return ADASUM_OK;
+}
+
+int check_ortho(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
+  if (count < 0 || count > kMaxOrthoCount) return fail(ADASUM_EINVAL, "count must be in [0, 2^16]");
+  if (rows < 0 || rows > kMaxOrthoSide || cols < 1 || cols > kMaxOrthoSide)
+    return fail(ADASUM_EINVAL, "orthogonalize: rows must be in [0, 2^15], cols in [1, 2^15]");
+  if (!known_dtype(out_dtype)) return fail(ADASUM_EINVAL, "unknown out_dtype");
+  return ADASUM_OK;
+}
+
+int64_t orthogonalize_bytes(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
+  RETURN_IF(check_ortho(count, rows, cols, out_dtype));
+  return count == 0 || rows == 0 ? 0 : (int64_t)ortho_layout(count, rows, cols, out_dtype).total;
+}
+
+// Follows the largest singular value through the steps: the kernels hold X and
+// B in fp16 parts, whose range they must not leave.
+int check_coefficients(int steps, const double* k) {
+  if (steps < 1 || steps > kOrthoSteps) return fail(ADASUM_EINVAL, "steps must be in [1, 16]");
+  if (k == nullptr) return fail(ADASUM_EINVAL, "coefficients is NULL");
+  double most = 1.001;  // with room for rounding
+  for (int s = 0; s < steps; ++s, k += 3) {
+    const double a = k[0], b = k[1], c = k[2], t = most * most;
+    if (!std::isfinite((float)a) || !std::isfinite((float)b) || !std::isfinite((float)c))
+      return fail(ADASUM_EINVAL, "coefficients must be finite in fp32");
+    auto image = [&](double u) { return std::fabs(std::sqrt(u) * (a + u * (b + u * c))); };  // of s^2 = u
+    auto added = [&](double u) { return std::fabs(u * (b + u * c)); };
+    double x = image(t), y = added(t);
+    // where a + 3 b u + 5 c u^2 = 0, and where b + 2 c u = 0
+    const double root = 9 * b * b - 20 * a * c;
+    double at[4] = {c != 0 && root >= 0 ? (-3 * b + std::sqrt(root)) / (10 * c) : 0,
+                    c != 0 && root >= 0 ? (-3 * b - std::sqrt(root)) / (10 * c) : 0, b != 0 ? -a / (3 * b) : 0,
+                    c != 0 ? -b / (2 * c) : 0};
+    for (double u : at)
+      if (u > 0 && u < t) {
+        x = std::max(x, image(u));
+        y = std::max(y, added(u));
+      }
+    if (!(x <= 1.9) || !(y <= 30.0))
+      return fail(ADASUM_EINVAL, "coefficients must keep singular values below 2, and b A + c A^2 below 31");
+    most = std::max(x * 1.01, 1e-3);
+  }
+  return ADASUM_OK;
+}
+
+int orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t cols, int64_t x_stride, int dtype,
+                  int steps, const double* coefficients, double eps, double scale, void* const* out,
+                  int64_t out_stride, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t x_bytes = 0, out_bytes = 0;
+  RETURN_IF(check_ortho(count, rows, cols, out_dtype));
+  RETURN_IF(check_matrix(rows, cols, x_stride, dtype, "x", &x_bytes));
+  RETURN_IF(check_matrix(rows, cols, out_stride, out_dtype, "out", &out_bytes));
+  RETURN_IF(check_coefficients(steps, coefficients));
+  if (!std::isfinite((float)eps) || (float)eps < FLT_MIN)
+    return fail(ADASUM_EINVAL, "eps must be a positive normal fp32 number");
+  if (!std::isfinite((float)scale)) return fail(ADASUM_EINVAL, "scale must be finite in fp32");
+  if (count == 0 || rows == 0) return ADASUM_OK;
+  if (x == nullptr || out == nullptr) return einval("%s is NULL", x == nullptr ? "x" : "out");
+  const size_t need = ortho_layout(count, rows, cols, out_dtype).total;
+  RETURN_IF(check_workspace(workspace, workspace_bytes, need));
+  std::vector<Buffer> b;
+  std::vector<int> index;
+  for (int64_t i = 0; i < count; ++i) {
+    const bool in_place = x[i] == out[i] && x_stride == out_stride && dtype == out_dtype;
+    b.push_back({x[i], in_place ? 0 : x_bytes, size_of(dtype), "x", false});
+    b.push_back({out[i], out_bytes, size_of(out_dtype), "out", true});
+    index.insert(index.end(), {(int)i, (int)i});
+  }
+  b.push_back({workspace, need, 16, "workspace", true});
+  index.push_back(-1);
+  RETURN_IF(check_many(b, index));
+  OrthoCall call{};
+  OrthoArgs& a = call.args;
+  a.rows = rows;
+  a.cols = cols;
+  a.x_stride = x_stride;
+  a.out_stride = out_stride;
+  a.out_dtype = out_dtype;
+  a.steps = steps;
+  a.eps = eps;
+  a.scale = (float)scale;
+  for (int i = 0; i < 3 * steps; ++i) a.coefficients[i] = (float)coefficients[i];
+  a.ws = static_cast<char*>(workspace);
+  call.count = count;
+  call.x = x;
+  call.out = out;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const double bytes = (double)count * rows * cols * (size_of(dtype) + size_of(out_dtype));
+  return launch(kOrthogonal, "orthogonalize", bytes, st, [&] { return launch_ortho(dtype, call, st); });
+}
+
 }  // namespace
 }  // namespace adasum
 
@@ -495,6 +865,70 @@ int adasum_linear_grad(const void* dy, int64_t rows, int64_t out_features, int64
   return adasum::guarded([&] {
     return adasum::linear_grad(dy, rows, out_features, dy_stride, dtype, codes, scales, in_features, dweight, dbias,
                                grad_dtype, accumulate, workspace, workspace_bytes, stream);
+  });
+}
+
+int adasum_rms(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, int dtype, const void* residual,
+               int64_t residual_stride, int stream_dtype, const void* weight, int param_dtype, double eps, void* y,
+               int64_t y_stride, void* h, int64_t h_stride, float* rstd, int8_t* codes, uint8_t* scales,
+               void* stream) {
+  return adasum::guarded([&] {
+    return adasum::rms(x, rows, hidden, x_stride, dtype, residual, residual_stride, stream_dtype, weight, param_dtype,
+                       eps, y, y_stride, h, h_stride, rstd, codes, scales, stream);
+  });
+}
+
+int64_t adasum_rms_grad_workspace_bytes(int64_t rows, int64_t hidden, int dtype) {
+  return adasum::guarded([&] { return adasum::rms_grad_bytes(rows, hidden, dtype); });
+}
+
+int adasum_rms_grad(const void* dy, int64_t rows, int64_t hidden, int64_t dy_stride, int dtype, const void* h,
+                    int64_t h_stride, int stream_dtype, const void* dh, int64_t dh_stride, const float* rstd,
+                    const void* weight, int param_dtype, void* dx, int64_t dx_stride, void* dweight, int grad_dtype,
+                    int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  return adasum::guarded([&] {
+    return adasum::rms_grad(dy, rows, hidden, dy_stride, dtype, h, h_stride, stream_dtype, dh, dh_stride, rstd, weight,
+                            param_dtype, dx, dx_stride, dweight, grad_dtype, accumulate, workspace, workspace_bytes,
+                            stream);
+  });
+}
+
+int adasum_relative_bias(const void* table, int64_t buckets, int64_t heads, int64_t table_stride, int table_dtype,
+                         int64_t max_distance, int bidirectional, int64_t batch, int64_t queries, int64_t keys,
+                         int64_t offset, const void* scores, int64_t scores_stride, void* out, int64_t out_stride,
+                         int dtype, void* stream) {
+  return adasum::guarded([&] {
+    return adasum::relative_bias(table, buckets, heads, table_stride, table_dtype, max_distance, bidirectional, batch,
+                                 queries, keys, offset, scores, scores_stride, out, out_stride, dtype, stream);
+  });
+}
+
+int64_t adasum_relative_bias_grad_workspace_bytes(int64_t batch, int64_t heads, int64_t queries, int64_t keys,
+                                                  int dtype) {
+  return adasum::guarded([&] { return adasum::relative_bias_grad_bytes(batch, heads, queries, keys, dtype); });
+}
+
+int adasum_relative_bias_grad(const void* dscores, int64_t batch, int64_t heads, int64_t queries, int64_t keys,
+                              int64_t stride, int dtype, int64_t offset, int64_t buckets, int64_t max_distance,
+                              int bidirectional, void* dtable, int grad_dtype, int accumulate, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  return adasum::guarded([&] {
+    return adasum::relative_bias_grad(dscores, batch, heads, queries, keys, stride, dtype, offset, buckets,
+                                      max_distance, bidirectional, dtable, grad_dtype, accumulate, workspace,
+                                      workspace_bytes, stream);
+  });
+}
+
+int64_t adasum_orthogonalize_workspace_bytes(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
+  return adasum::guarded([&] { return adasum::orthogonalize_bytes(count, rows, cols, out_dtype); });
+}
+
+int adasum_orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t cols, int64_t x_stride, int dtype,
+                         int steps, const double* coefficients, double eps, double scale, void* const* out,
+                         int64_t out_stride, int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return adasum::guarded([&] {
+    return adasum::orthogonalize(x, count, rows, cols, x_stride, dtype, steps, coefficients, eps, scale, out,
+                                 out_stride, out_dtype, workspace, workspace_bytes, stream);
   });
 }
 

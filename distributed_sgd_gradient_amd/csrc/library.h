@@ -81,7 +81,7 @@ bool log_enabled();
 
 // Launch timing (adasum_profile_begin): the events around one record.  Caller
 // holds g_mu.
-enum KernelKind { kGram = 0, kTree, kWsum, kSum, kExact, kEmbedding, kNorm, kPack, kLinear, kNumKinds };
+enum KernelKind { kGram = 0, kTree, kWsum, kSum, kExact, kEmbedding, kNorm, kPack, kLinear, kBias, kOrthogonal, kNumKinds };
 int prof_start(int kind, double bytes, hipStream_t st);
 void prof_stop(int idx, hipStream_t st);
 

@@ -1,0 +1,335 @@
+// relative_bias.hip - a learned bias of attention scores by the distance
+// between query and key, and its table's gradient.
+//
+//   forward    out[n][h][i][j] = scores[n][h][i][j] + table[bucket(d)][h],
+//              d = j - i - offset
+//   gradient   dtable[b][h] = sum over n, i, j with bucket(d) = b of
+//              dscores[n][h][i][j]
+//
+// A head's bias depends on d alone.  The forward pass puts the line of all d of
+// its tile in LDS once, and every row of the tile and of the batch is a piece of
+// it.  The gradient first sums along the diagonals of the score matrices: a lane
+// owns a vector of neighbouring diagonals and walks down the rows, its column
+// moving on by one each row, so the sums stay in registers (loads need no
+// alignment on gfx950, and the lanes of a wave read neighbouring vectors).
+// Buckets are runs of diagonals, summed by a second kernel.  Both are bound by
+// HBM.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <vector>
+
+#include "elem.h"
+#include "layer_ops.h"
+
+namespace adasum {
+namespace {
+
+using namespace elem;
+
+constexpr int kTileRows = 16, kTileCols = 1024;  // of the forward pass
+constexpr int kPieces = 4;                       // pieces a lane has in flight
+constexpr int kGradUnit = 64, kGradAhead = 8;    // rows of a unit, rows in flight
+
+// The bucket of distance n on its side: the last border at or below n.
+__device__ __forceinline__ int bucket_of(const BiasBuckets& k, uint32_t n) {
+  int lo = 0, hi = k.side;  // border[lo] <= n < border[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (k.border[mid] <= n)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The table's row for distance d = key - query.
+__device__ __forceinline__ int bucket_at(const BiasBuckets& k, int64_t d) {
+  const int64_t n = k.both ? (d < 0 ? -d : d) : (d < 0 ? -d : 0);
+  const int b = bucket_of(k, (uint32_t)min<int64_t>(n, 0x7fffffff));
+  return k.both && d > 0 ? b + k.side : b;
+}
+
+// A step of nine words for eight values keeps the lanes' pieces of the line in
+// different banks.
+__device__ __forceinline__ int line_at(int k) { return k + (k >> 3); }
+
+template <typename T, bool ADD>
+__global__ __launch_bounds__(256) void bias_kernel(BiasArgs a, BiasLayout l) {
+  constexpr int VEC = Type<T>::kVec;
+  __shared__ float line[(kTileRows + kTileCols) * 9 / 8 + 1];
+  uint32_t block = blockIdx.x;
+  const int64_t col_tile = block % l.col_tiles;
+  block /= l.col_tiles;
+  const int64_t row_tile = block % l.row_tiles;
+  block /= l.row_tiles;
+  const int64_t head = block % a.heads, part = block / a.heads;
+  const int64_t i0 = row_tile * kTileRows, j0 = col_tile * kTileCols;
+  const int rows = (int)min<int64_t>(kTileRows, a.queries - i0), cols = (int)min<int64_t>(kTileCols, a.keys - j0);
+  // line[k] is the bias at key - query = first + k
+  const int64_t first = j0 - (i0 + rows - 1) - a.offset;
+  for (int k = threadIdx.x; k < rows + cols - 1; k += 256)
+    line[line_at(k)] = load_any(a.table, a.table_dtype, (int64_t)bucket_at(a.buckets, first + k) * a.table_stride + head);
+  __syncthreads();
+  const int64_t n_begin = part * l.part_batch, n_end = min(a.batch, n_begin + l.part_batch);
+  const uint32_t per_row = (uint32_t)(cols + VEC - 1) / VEC, per_batch = per_row * rows;
+  // below 2^30: bias_layout leaves a workgroup 1 / 2048 of 2^40 elements at most
+  const uint32_t total = (uint32_t)(n_end - n_begin) * per_batch;
+  const T* scores = static_cast<const T*>(a.scores);
+  T* out = static_cast<T*>(a.out);
+  for (uint32_t p0 = 0; p0 < total; p0 += 256 * kPieces) {
+    v4u raw[kPieces];
+    int64_t row[kPieces];
+    int col[kPieces], at[kPieces], valid[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const uint32_t p = p0 + u * 256 + threadIdx.x, n = p / per_batch, q = p - n * per_batch, r = q / per_row;
+      col[u] = (int)(q - r * per_row) * VEC;
+      row[u] = ((n_begin + n) * a.heads + head) * a.queries + i0 + r;
+      at[u] = rows - 1 - (int)r + col[u];
+      valid[u] = p < total ? cols - col[u] : 0;
+      if constexpr (ADD) raw[u] = load_raw(scores + row[u] * a.scores_stride + j0 + col[u], valid[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      float v[VEC];
+      if constexpr (ADD) widen<T>(raw[u], v);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float b = e < valid[u] ? line[line_at(at[u] + e)] : 0.f;
+        v[e] = ADD ? v[e] + b : b;
+      }
+      store_vec(out + row[u] * a.out_stride + j0 + col[u], v, valid[u]);
+    }
+  }
+}
+
+// Sums along diagonals.  Diagonal D = j - i + queries - 1; LPD lanes own VEC
+// diagonals each, and a wave's 64 / LPD groups, like the four waves, take units
+// of kGradUnit rows of a sequence in turn.
+template <typename T, int LPD>
+__global__ __launch_bounds__(256) void bias_grad_kernel(BiasGradArgs a, BiasGradLayout l) {
+  constexpr int VEC = Type<T>::kVec, GROUPS = 256 / LPD;
+  const int lane = threadIdx.x & (LPD - 1), group = threadIdx.x / LPD;
+  uint32_t block = blockIdx.x;
+  const int64_t tile = block % l.tiles;
+  block /= l.tiles;
+  const int64_t head = block % a.heads, split = block / a.heads;
+  const int64_t diagonals = a.queries + a.keys - 1;
+  const int64_t d0 = (tile * LPD + lane) * VEC;
+  const int64_t shift = d0 - (a.queries - 1);  // column of the lane's first diagonal in row 0
+  const T* base = static_cast<const T*>(a.dscores);
+  const int64_t all_rows = a.batch * a.heads * a.queries;
+  const int64_t extent = (all_rows - 1) * a.stride + a.keys;  // elements from the first to the last
+  const int64_t row_units = (a.queries + kGradUnit - 1) / kGradUnit, units = a.batch * row_units;
+  float acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  const int64_t last_start = extent - VEC;  // where a vector may start at most; below 0: none may
+  for (int64_t unit = split * GROUPS + group; unit < units; unit += (int64_t)l.splits * GROUPS) {
+    const int64_t n = unit / row_units, begin = (unit - n * row_units) * kGradUnit;
+    const int64_t end = min(a.queries, begin + kGradUnit);
+    // rows in which any of the tile's diagonals has a column
+    const int64_t tile_shift = tile * LPD * VEC - (a.queries - 1);
+    const int64_t lo = max(begin, -(tile_shift + LPD * VEC - 1)), hi = min(end, a.keys - tile_shift);
+    const int64_t row0 = (n * a.heads + head) * a.queries;
+    for (int64_t i0 = lo; i0 < hi; i0 += kGradAhead) {
+      v4u raw[kGradAhead];
+#pragma unroll
+      for (int u = 0; u < kGradAhead; ++u) {
+        // A vector that reaches over its row's ends reads its neighbours in
+        // memory, whose values are dropped below; one that lies outside its
+        // row, or would leave the matrix, reads the row's own first (or the
+        // last possible) vector.  No branch: all loads are on their way at once.
+        const int64_t i = i0 + u, j = shift + i;
+        const int64_t start = (row0 + min(i, hi - 1)) * a.stride;
+        int64_t at = start + j;
+        if (i >= hi || j <= -VEC || j >= a.keys) at = start;
+        at = max<int64_t>(0, min(at, last_start));
+        raw[u] = last_start >= 0 ? load_at<v4u, sizeof(T)>(base + at) : v4u{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int u = 0; u < kGradAhead; ++u) {
+        const int64_t i = i0 + u, j = shift + i, at = (row0 + i) * a.stride + j;
+        const bool there = i < hi && at >= 0 && at <= last_start;
+        float v[VEC];
+        widen<T>(raw[u], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += there && j + e >= 0 && j + e < a.keys ? v[e] : 0.f;
+        if (i < hi && !there) {  // the matrix's first and last row
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (j + e >= 0 && j + e < a.keys) acc[e] += (float)base[at + e];
+        }
+      }
+    }
+  }
+  // the groups' sums, added in their order
+  __shared__ float part[256 * VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) part[e * 256 + threadIdx.x] = acc[e];
+  __syncthreads();
+  if (group == 0) {
+    float* out = a.partials + (split * a.heads + head) * diagonals;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) s += part[e * 256 + g * LPD + lane];
+      if (d0 + e < diagonals) out[d0 + e] = s;
+    }
+  }
+}
+
+// dtable[b][h]: bucket b's diagonals of every split, summed in fp64 by a
+// workgroup in a fixed order.
+__global__ __launch_bounds__(256) void bias_join_kernel(BiasGradArgs a, int splits) {
+  __shared__ double sums[256];
+  const int64_t head = blockIdx.x % (uint32_t)a.heads;
+  const int b = blockIdx.x / (uint32_t)a.heads;
+  const BiasBuckets& k = a.buckets;
+  const bool ahead = k.both && b >= k.side;  // keys behind the query
+  const int s = ahead ? b - k.side : b;
+  const int64_t near = k.border[s], far = s + 1 < k.side ? k.border[s + 1] : int64_t(1) << 40;  // near <= n < far
+  // as key - query, both ends included
+  int64_t lo, hi;
+  if (ahead) {
+    lo = max<int64_t>(near, 1);
+    hi = far - 1;
+  } else {
+    lo = -(far - 1);
+    hi = !k.both && s == 0 ? int64_t(1) << 40 : -near;
+  }
+  const int64_t diagonals = a.queries + a.keys - 1, zero = a.queries - 1 + a.offset;
+  lo = max<int64_t>(lo + zero, 0);
+  hi = min(hi + zero, diagonals - 1);
+  const int64_t width = hi - lo + 1;
+  double t = 0.0;
+  if (width > 0) {
+    const int64_t count = width * splits;
+    for (int64_t p = threadIdx.x; p < count; p += 256) {
+      const int64_t q = p / width;
+      t += (double)a.partials[(q * a.heads + head) * diagonals + lo + (p - q * width)];
+    }
+  }
+  sums[threadIdx.x] = t;
+  __syncthreads();
+  for (int w = 128; w > 0; w /= 2) {
+    if ((int)threadIdx.x < w) sums[threadIdx.x] += sums[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const int64_t i = (int64_t)b * a.heads + head;
+    const double sum = sums[0];
+    store_any(a.dtable, a.grad_dtype, i, a.accumulate ? sum + (double)load_any(a.dtable, a.grad_dtype, i) : sum);
+  }
+}
+
+// Whole numbers of any size, for borders that are powers.
+typedef std::vector<uint32_t> Whole;
+void times(Whole* w, uint32_t f) {
+  uint64_t carry = 0;
+  for (uint32_t& x : *w) {
+    carry += (uint64_t)x * f;
+    x = (uint32_t)carry;
+    carry >>= 32;
+  }
+  if (carry) w->push_back((uint32_t)carry);
+}
+Whole product(uint32_t x, int times_x, uint32_t y, int times_y) {
+  Whole w{1u};
+  for (int i = 0; i < times_x; ++i) times(&w, x);
+  for (int i = 0; i < times_y; ++i) times(&w, y);
+  return w;
+}
+bool at_least(const Whole& a, const Whole& b) {
+  if (a.size() != b.size()) return a.size() > b.size();
+  for (size_t i = a.size(); i-- > 0;)
+    if (a[i] != b[i]) return a[i] > b[i];
+  return true;
+}
+
+}  // namespace
+
+// border[k] is the least n with (n / e)^(m - e) >= (reach / e)^(k - e), decided
+// in whole numbers where the quotient of logarithms cannot.
+BiasBuckets bias_buckets(int buckets, int64_t reach, bool both) {
+  BiasBuckets t{};
+  t.both = both;
+  t.side = both ? buckets / 2 : buckets;
+  const int m = t.side, e = m / 2;
+  for (int k = 0; k < m; ++k) {
+    if (k <= e) {
+      t.border[k] = (uint32_t)k;
+      continue;
+    }
+    const double x = e * std::pow((double)reach / e, (double)(k - e) / (m - e)), near = std::nearbyint(x);
+    uint32_t n = (uint32_t)std::ceil(x);
+    if (std::fabs(x - near) <= 1e-9 * x) {
+      n = (uint32_t)near;
+      if (!at_least(product(n, m - e, (uint32_t)e, k - e), product((uint32_t)reach, k - e, (uint32_t)e, m - e))) ++n;
+    }
+    t.border[k] = n;
+  }
+  return t;
+}
+
+BiasLayout bias_layout(int64_t batch, int64_t heads, int64_t queries, int64_t keys) {
+  BiasLayout l{};
+  l.row_tiles = ceil_div(queries, kTileRows);
+  l.col_tiles = ceil_div(keys, kTileCols);
+  const int64_t tiles = l.row_tiles * l.col_tiles * heads;
+  // a workgroup keeps its line for as many sequences as leave 2048 workgroups
+  const int64_t parts = std::min(batch, std::max<int64_t>(1, ceil_div(2048, tiles)));
+  l.part_batch = ceil_div(batch, parts);
+  l.blocks = tiles * ceil_div(batch, l.part_batch);
+  return l;
+}
+
+hipError_t launch_bias(int dtype, const BiasArgs& a, hipStream_t st) {
+  const BiasLayout l = bias_layout(a.batch, a.heads, a.queries, a.keys);
+  return with_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    if (a.scores)
+      bias_kernel<T, true><<<(unsigned)l.blocks, 256, 0, st>>>(a, l);
+    else
+      bias_kernel<T, false><<<(unsigned)l.blocks, 256, 0, st>>>(a, l);
+    return hipGetLastError();
+  });
+}
+
+BiasGradLayout bias_grad_layout(int64_t batch, int64_t heads, int64_t queries, int64_t keys, int dtype) {
+  BiasGradLayout l{};
+  const int vec = dtype == 0 ? 4 : 8;
+  const int64_t diagonals = queries + keys - 1;
+  l.lanes = diagonals <= 32 * vec ? 16 : 64;
+  l.tiles = ceil_div(diagonals, l.lanes * vec);
+  const int64_t units = batch * ceil_div(queries, kGradUnit), groups = 256 / l.lanes;
+  // as many workgroups as fill the card twice, each group with a unit at least;
+  // and no more than 64 units, 4096 rows, in one fp32 sum
+  const int64_t fill = ceil_div(2 * 4 * kCUs, l.tiles * heads), most = ceil_div(units, groups);
+  l.splits = std::max<int64_t>({1, std::min(fill, most), ceil_div(units, groups * 64)});
+  l.blocks = l.splits * heads * l.tiles;
+  l.bytes = (size_t)l.splits * heads * diagonals * sizeof(float);
+  return l;
+}
+
+hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st) {
+  const BiasGradLayout l = bias_grad_layout(a.batch, a.heads, a.queries, a.keys, dtype);
+  const hipError_t e = with_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    if (l.lanes == 16)
+      bias_grad_kernel<T, 16><<<(unsigned)l.blocks, 256, 0, st>>>(a, l);
+    else
+      bias_grad_kernel<T, 64><<<(unsigned)l.blocks, 256, 0, st>>>(a, l);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  bias_join_kernel<<<(unsigned)(a.buckets_total * a.heads), 256, 0, st>>>(a, (int)l.splits);
+  return hipGetLastError();
+}
+
+}  // namespace adasum

@@ -1,8 +1,8 @@
 """Python front end of the layer operators: what a worker computes from its
 microbatch before its gradient is combined with the others'.
 
-Embedding lookup, layer norm, activations kept in 8 bits, and the gradients of
-the tables and weights, which may be written straight into (or added to) the
+Embedding lookup, layer norm, the norm of a residual stream, relative position
+biases, activations kept in 8 bits, and the gradients of the tables and weights, which may be written straight into (or added to) the
 segments of a flat gradient buffer that :func:`combine` reads.  As there, only
 argument marshalling happens here; torch provides device memory and streams.
 
@@ -357,6 +357,226 @@ def layer_norm_keep_grad(dy, codes, scales, rstd, weight=None, *, dx=None, dweig
     arguments and results as for :func:`layer_norm_grad`."""
     return _norm_grad(dy, None, None, codes, scales, rstd, weight, dx, dweight, dbias, bias, accumulate, workspace,
                       stream)
+
+
+def _rms(x, weight, residual, eps, out, h, stream, pack, values):
+    dev = _on(x, "x").device
+    rows, hidden, stride = _rows(x, "x")
+    code = _code(x.dtype, "x")
+    param_code = _param(weight, "weight", dev, hidden) if weight is not None else 0
+    stream_code, res_stride, h_stride = code, hidden, hidden
+    if residual is not None:
+        _on(residual, "residual", dev)
+        if residual.shape != x.shape or residual.dtype not in (x.dtype, torch.float32):
+            raise ValueError("residual must have the shape of x, and its dtype or float32")
+        stream_code = _code(residual.dtype, "residual")
+        res_stride = _rows(residual, "residual")[2]
+        if h is not None:
+            _like(h, "h", dev, x.shape, residual.dtype)
+            h_stride = _rows(h, "h")[2]
+    elif h is not None:
+        raise ValueError("without a residual there is no h: it is x")
+    out_stride = hidden
+    if out is not None:
+        if not values:
+            raise ValueError("out is for y, which values=False leaves out")
+        _like(out, "out", dev, x.shape, x.dtype)
+        out_stride = _rows(out, "out")[2]
+
+    def body(st):
+        y = out
+        if values and y is None:
+            y = _fresh(x, x.dtype)
+        total = h
+        if residual is not None and total is None:
+            total = _fresh(x, residual.dtype)
+        lead = _lead(x, rows)
+        rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+        codes = scales = None
+        if pack:
+            codes = _fresh(x, torch.int8)
+            scales = torch.empty((*lead, _blocks(hidden)), dtype=torch.uint8, device=dev)
+        _native.check(_native.lib().adasum_rms(
+            x.data_ptr(), rows, hidden, stride, code, _ptr(residual), res_stride, stream_code, _ptr(weight), param_code,
+            eps, _ptr(y), out_stride, _ptr(total), h_stride, rstd.data_ptr(), _ptr(codes), _ptr(scales), st))
+        total = x if residual is None else total
+        return (y, codes, scales, total, rstd) if pack else (y, total, rstd)
+    return _call(dev, stream, body)
+
+
+def rms_norm(x, weight=None, *, residual=None, eps=1e-6, out=None, h=None, stream=None):
+    """Root-mean-square norm of h = x + residual over the last dimension (at
+    most 16384 wide): (y, h, rstd) with y = h * rstd * weight, of x's dtype, and
+    rstd = 1 / sqrt(mean(h^2) + eps) in fp32 for :func:`rms_norm_grad`.
+
+    residual: like x, or float32 beside a 16-bit x; h has its dtype and is what
+    y is formed from, as it is stored.  h may be the residual itself: the stream
+    is then updated in place.  Without a residual h is x.  weight: [hidden], or
+    None (1).
+    """
+    return _rms(x, weight, residual, eps, out, h, stream, False, True)
+
+
+def rms_norm_pack(x, weight=None, *, residual=None, eps=1e-6, values=True, out=None, h=None, stream=None):
+    """:func:`rms_norm` that gives y in 8 bits too: (y, codes, scales, h, rstd),
+    codes and scales being those of ``checkpoint_pack(y)``, which
+    :func:`linear_grad` takes.  With values=False y is given in 8 bits only (and
+    None in its place)."""
+    return _rms(x, weight, residual, eps, out, h, stream, True, values)
+
+
+def rms_norm_grad(dy, h, rstd, weight=None, *, dh=None, dx=None, dweight=None, accumulate=False, workspace=None,
+                  stream=None):
+    """Backward pass of :func:`rms_norm`: (dx, dweight), dx being the gradient
+    of x and of the residual alike, of h's dtype; dweight None without weight.
+
+    dh: the gradient that reaches h past the norm, along the residual stream (of
+    h's shape and dtype), added to dx; dx may be dh itself.  dweight has the
+    dtype of weight, or of the tensor given for it (a segment of a gradient
+    buffer), to which it is added with accumulate.
+    """
+    dev = _on(dy, "dy").device
+    rows, hidden, stride = _rows(dy, "dy")
+    code = _code(dy.dtype, "dy")
+    _on(h, "h", dev)
+    if h.shape != dy.shape or h.dtype not in (dy.dtype, torch.float32):
+        raise ValueError("h must have the shape of dy, and its dtype or float32")
+    stream_code = _code(h.dtype, "h")
+    h_stride = _rows(h, "h")[2]
+    _dense(rstd, "rstd", dev, (rows,), torch.float32)
+    param_code = _param(weight, "weight", dev, hidden) if weight is not None else 0
+    dh_stride = dx_stride = hidden
+    if dh is not None:
+        _like(dh, "dh", dev, h.shape, h.dtype)
+        dh_stride = _rows(dh, "dh")[2]
+    if dx is not None:
+        _like(dx, "dx", dev, h.shape, h.dtype)
+        dx_stride = _rows(dx, "dx")[2]
+    if weight is None and dweight is not None:
+        raise ValueError("a norm without weight has no dweight")
+    if accumulate and dweight is None:
+        raise ValueError("accumulate needs dweight")
+    grad_dtype = torch.float32
+    if weight is not None:
+        grad_dtype = weight.dtype if dweight is None else dweight.dtype
+    if dweight is not None:
+        _dense(dweight, "dweight", dev, (hidden,))
+    grad_code = _code(grad_dtype, "dweight")
+    L = _native.lib()
+    need = _native.check(L.adasum_rms_grad_workspace_bytes(rows, hidden, code)) if weight is not None else 0
+
+    def body(st):
+        ws = _workspace(workspace, need, dev)
+        d = _fresh(h, h.dtype) if dx is None else dx
+        dw = dweight
+        if weight is not None and dw is None:
+            dw = torch.empty(hidden, dtype=grad_dtype, device=dev)
+        _native.check(L.adasum_rms_grad(
+            dy.data_ptr(), rows, hidden, stride, code, h.data_ptr(), h_stride, stream_code, _ptr(dh), dh_stride,
+            rstd.data_ptr(), _ptr(weight), param_code, d.data_ptr(), dx_stride, _ptr(dw), grad_code, int(accumulate),
+            _ptr(ws), _size(ws), st))
+        return d, dw
+    return _call(dev, stream, body)
+
+
+def _scores(t, name):
+    """(batch, heads, queries, keys, row stride) of [..., heads, queries, keys]."""
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be [..., heads, queries, keys]")
+    heads, queries = t.size(-3), t.size(-2)
+    if heads < 1:
+        raise ValueError(f"{name} needs a head at least")
+    batch = 1
+    for n in t.shape[:-3]:
+        batch *= n
+    _, keys, stride = _rows(t, name)
+    return batch, heads, queries, keys, stride
+
+
+def relative_bias(table, queries=None, keys=None, *, scores=None, offset=0, bidirectional=True, max_distance=128,
+                  dtype=None, out=None, stream=None):
+    """A learned bias of attention scores by the distance d = j - i - offset
+    between key j and query i: table[bucket(d), h] for head h.
+
+    table: [buckets, heads], at most 256 buckets.  Without scores the result is
+    [heads, queries, keys] of ``dtype`` (default: the table's); with scores
+    [..., heads, queries, keys] it is scores plus the bias, of the scores' dtype,
+    and out may be the scores themselves.  offset: the position of the first
+    query among the keys (for one new token, the number of keys before it).
+
+    bidirectional: half of the buckets are for keys behind the query (d > 0);
+    otherwise those count as distance 0.  With m buckets on a side and e = m // 2,
+    distances n below e have one bucket each, those from e on bucket
+    e + floor(log(n / e) / log(max_distance / e) * (m - e)), at most m - 1; borders
+    that are whole numbers are met exactly.
+    """
+    dev = _on(table, "table").device
+    if table.dim() != 2:
+        raise ValueError("table must be [buckets, heads]")
+    buckets, heads, stride = _rows(table, "table")
+    scores_stride = 0
+    if scores is not None:
+        _on(scores, "scores", dev)
+        if queries is not None or keys is not None:
+            raise ValueError("scores have their own queries and keys")
+        if dtype is not None and dtype != scores.dtype:
+            raise ValueError("the result has the dtype of scores")
+        dtype, shape = scores.dtype, tuple(scores.shape)
+        batch, have, queries, keys, scores_stride = _scores(scores, "scores")
+        if have != heads:
+            raise ValueError(f"scores have {have} heads, table has {heads}")
+    else:
+        if queries is None or keys is None or queries < 0 or keys < 1:
+            raise ValueError("without scores, queries and keys (at least one) are needed")
+        if dtype is None:
+            dtype = table.dtype if out is None else out.dtype
+        batch, shape = 1, (heads, queries, keys)
+    out_stride = keys
+    if out is not None:
+        _like(out, "out", dev, shape, dtype)
+        out_stride = _rows(out, "out")[2]
+    codes = _code(table.dtype, "table"), _code(dtype, "out")
+
+    def body(st):
+        y = torch.empty(shape, dtype=dtype, device=dev) if out is None else out
+        _native.check(_native.lib().adasum_relative_bias(
+            table.data_ptr(), buckets, heads, stride, codes[0], max_distance, int(bidirectional), batch, queries, keys,
+            offset, _ptr(scores), scores_stride, y.data_ptr(), out_stride, codes[1], st))
+        return y
+    return _call(dev, stream, body)
+
+
+def relative_bias_grad(dscores, buckets, *, offset=0, bidirectional=True, max_distance=128, dtype=None, out=None,
+                       accumulate=False, workspace=None, stream=None):
+    """The gradient [buckets, heads] of :func:`relative_bias`'s table: per
+    bucket and head the sum of dscores [..., heads, queries, keys] over all
+    leading dimensions, queries and keys.
+
+    dtype: of the gradient (default: dscores').  out: a contiguous tensor of
+    buckets * heads elements, for instance a segment of a gradient buffer; with
+    accumulate the gradient is added to it.
+    """
+    dev = _on(dscores, "dscores").device
+    batch, heads, queries, keys, stride = _scores(dscores, "dscores")
+    code = _code(dscores.dtype, "dscores")
+    if out is not None:
+        _dense(out, "out", dev, (buckets, heads), dtype)
+        dtype = out.dtype
+    elif accumulate:
+        raise ValueError("accumulate needs out")
+    dtype = dscores.dtype if dtype is None else dtype
+    grad_code = _code(dtype, "out")
+    L = _native.lib()
+    need = _native.check(L.adasum_relative_bias_grad_workspace_bytes(batch, heads, queries, keys, code))
+
+    def body(st):
+        ws = _workspace(workspace, need, dev)
+        grad = torch.empty((buckets, heads), dtype=dtype, device=dev) if out is None else out
+        _native.check(L.adasum_relative_bias_grad(
+            dscores.data_ptr(), batch, heads, queries, keys, stride, code, offset, buckets, max_distance,
+            int(bidirectional), grad.data_ptr(), grad_code, int(accumulate), _ptr(ws), _size(ws), st))
+        return grad
+    return _call(dev, stream, body)
 
 
 def checkpoint_pack(x, *, codes=None, scales=None, stream=None):

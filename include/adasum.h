@@ -367,6 +367,120 @@ ADASUM_API int adasum_linear_grad(const void* dy, int64_t rows, int64_t out_feat
                                   size_t workspace_bytes, void* stream);
 
 /*
+ * adasum_rms - root-mean-square norm of a residual stream's rows:
+ * h = x + residual, rounded to the stream's type, rstd = 1 / sqrt(mean(h^2) +
+ * eps), y = h * rstd * weight.  Where a row's squares pass fp32's range, rstd
+ * is 0.
+ *
+ *   x, y         rows x hidden elements of dtype, hidden <= 16384.
+ *   residual, h  rows x hidden elements of stream_dtype: dtype or fp32.  h may
+ *                be NULL, and may be the residual (with its stride): updated in
+ *                place.  residual NULL: h is x, the argument h NULL and
+ *                stream_dtype dtype.
+ *   weight       hidden elements of param_dtype; NULL: 1.
+ *   eps          a positive normal fp32 number.
+ *   rstd         rows fp32 values, for the backward pass.
+ *   codes, scales
+ *                NULL, or where y is given in 8 bits too: what
+ *                adasum_checkpoint_pack gives for y.  y may be NULL then.
+ */
+ADASUM_API int adasum_rms(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, int dtype,
+                          const void* residual, int64_t residual_stride, int stream_dtype, const void* weight,
+                          int param_dtype, double eps, void* y, int64_t y_stride, void* h, int64_t h_stride,
+                          float* rstd, int8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * adasum_rms_grad - the backward pass.  With g = dy * weight and n = h * rstd:
+ *   dx      = dh + rstd * (g - n * mean(g * n)), the mean over a row: the
+ *             gradient of x and of the residual;
+ *   dweight = sum over rows of dy * n.
+ *
+ *   dy           rows x hidden elements of dtype.
+ *   h, dh, dx    rows x hidden elements of stream_dtype: dtype or fp32.  dh (the
+ *                gradient that reaches h along the residual stream) may be NULL:
+ *                0; dx may be dh (with its stride).
+ *   dweight      hidden elements of grad_dtype; NULL: not wanted.
+ *   workspace    adasum_rms_grad_workspace_bytes(...) bytes; may be NULL where
+ *                dweight is not wanted.
+ */
+ADASUM_API int64_t adasum_rms_grad_workspace_bytes(int64_t rows, int64_t hidden, int dtype);
+ADASUM_API int adasum_rms_grad(const void* dy, int64_t rows, int64_t hidden, int64_t dy_stride, int dtype,
+                               const void* h, int64_t h_stride, int stream_dtype, const void* dh, int64_t dh_stride,
+                               const float* rstd, const void* weight, int param_dtype, void* dx, int64_t dx_stride,
+                               void* dweight, int grad_dtype, int accumulate, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * adasum_relative_bias - a learned bias of attention scores by distance:
+ * out[n][h][i][j] = scores[n][h][i][j] + table[bucket(d)][h], d = j - i -
+ * offset.
+ *
+ * bidirectional: m = buckets / 2 buckets for d <= 0 and as many, from m on, for
+ * d > 0; otherwise m = buckets, and d > 0 counts as 0.  With e = m / 2 (whole),
+ * a distance n = |d| has bucket n below e, and from e on
+ * e + floor(log(n / e) / log(max_distance / e) * (m - e)), at most m - 1.
+ * Borders that are whole numbers are met exactly.
+ *
+ *   table        buckets rows of heads elements of table_dtype; 2 to 256
+ *                buckets (in both directions an even number from 4 on).
+ *   max_distance above e, at most 2^30.
+ *   offset       the place of the first query among the keys, within 2^31.
+ *   scores, out  batch x heads x queries rows of keys elements of dtype.
+ *                scores NULL: the bias alone; out may be scores (with its
+ *                stride).
+ */
+ADASUM_API int adasum_relative_bias(const void* table, int64_t buckets, int64_t heads, int64_t table_stride,
+                                    int table_dtype, int64_t max_distance, int bidirectional, int64_t batch,
+                                    int64_t queries, int64_t keys, int64_t offset, const void* scores,
+                                    int64_t scores_stride, void* out, int64_t out_stride, int dtype, void* stream);
+
+/*
+ * adasum_relative_bias_grad - the table's gradient:
+ * dtable[b][h] = sum over n, i and j with bucket(j - i - offset) = b of
+ * dscores[n][h][i][j].  Sums are fp32 over at most 4096 rows, joined in fp64,
+ * in a fixed order.
+ *
+ *   dscores      batch x heads x queries rows of keys elements of dtype.
+ *   dtable       dense, buckets x heads elements of grad_dtype.
+ *   workspace    adasum_relative_bias_grad_workspace_bytes(...) bytes.
+ */
+ADASUM_API int64_t adasum_relative_bias_grad_workspace_bytes(int64_t batch, int64_t heads, int64_t queries,
+                                                             int64_t keys, int dtype);
+ADASUM_API int adasum_relative_bias_grad(const void* dscores, int64_t batch, int64_t heads, int64_t queries,
+                                         int64_t keys, int64_t stride, int dtype, int64_t offset, int64_t buckets,
+                                         int64_t max_distance, int bidirectional, void* dtable, int grad_dtype,
+                                         int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * adasum_orthogonalize - what becomes of a combined gradient: its matrices
+ * brought near the closest orthogonal ones.  X = x[k] / (Frobenius norm + eps);
+ * then, steps times, X = a X + (b A + c A A) X with A = X X^T (where rows >
+ * cols, of the transposes); out[k] = scale * X.  A matrix that holds an
+ * infinity or NaN becomes NaN, one of zeros stays zero.
+ *
+ *   x, out       host arrays of count pointers to matrices of rows x cols
+ *                elements of dtype and out_dtype, rows x_stride and out_stride
+ *                apart.  out[k] may be x[k] (with its stride and type).  Sides
+ *                are at most 2^15, count at most 2^16.
+ *   coefficients host array: steps (1 to 16) times a, b, c.  Refused unless they
+ *                keep singular values of up to 1 below 2 (1.9, followed through
+ *                the steps), and |b s^2 + c s^4| below 31 (30).
+ *   eps          a positive normal fp32 number.
+ *   scale        finite in fp32.
+ *   workspace    adasum_orthogonalize_workspace_bytes(...) bytes.
+ *
+ * Operands of the products are fp16, their sums fp32; X itself has 22 bits.
+ * bf16 results take one part of each operand (off by some 0.15 % of the norm,
+ * as much as their rounding), fp32 and fp16 results two (off by less than
+ * products of fp32 values).
+ */
+ADASUM_API int64_t adasum_orthogonalize_workspace_bytes(int64_t count, int64_t rows, int64_t cols, int out_dtype);
+ADASUM_API int adasum_orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t cols, int64_t x_stride,
+                                    int dtype, int steps, const double* coefficients, double eps, double scale,
+                                    void* const* out, int64_t out_stride, int out_dtype, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
  * Kernel timing, for benchmarks.  Between adasum_profile_begin() and
  * adasum_profile_end(), every kernel launch that any combine call of this
  * process enqueues (and the launches of every layer operator's call, as one)
@@ -381,8 +495,9 @@ ADASUM_API int adasum_linear_grad(const void* dy, int64_t rows, int64_t out_feat
 typedef struct {
   char kernel[32];     /* "gram", "tree", "exact", "wsum" (a small combine's
                           fused walk and weighted sum counts here), "sum";
-                          of the layer operators "embedding", "norm", "pack"
-                          and "linear", one count and one duration a call */
+                          of the layer operators "embedding", "norm", "pack",
+                          "linear", "bias" and "orthogonal", one count and one
+                          duration a call */
   int launches;
   double milliseconds;
   double bytes;

@@ -331,3 +331,12 @@ __forceinline__ C on_cpu_multiply(V a, V b, C c) {
 }
 #define __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, x, y, z) on_cpu_multiply(a, b, c)
 #define __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, x, y, z) on_cpu_multiply(a, b, c)
+
+// A wave's 64 pieces of 16 bytes from anywhere to consecutive places in LDS.
+template <typename G, typename L>
+__forceinline__ void on_cpu_load_lds(G from, L to) {
+  std::memcpy((char*)to + 16 * on_cpu::lane_id(), (const char*)from, 16);
+}
+#define __builtin_amdgcn_global_load_lds(from, to, bytes, offset, aux) on_cpu_load_lds(from, to)
+#define __builtin_amdgcn_s_waitcnt(counts) ((void)0)
+#define __builtin_amdgcn_s_barrier() on_cpu::wait(on_cpu::kBarrier)
