@@ -22,7 +22,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libadasum.so")
 
 SOURCES = ["adasum.hip", "kernels.hip", "noalloc.hip", "plan.cpp", "layer_ops.hip", "embedding.hip", "layer_norm.hip",
-           "checkpoint.hip", "linear_grad.hip", "rms.hip", "relative_bias.hip", "orthogonal.hip"]
+           "checkpoint.hip", "linear_grad.hip", "rms.hip", "relative_bias.hip", "orthogonal.hip",
+           "orthogonal_narrow.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

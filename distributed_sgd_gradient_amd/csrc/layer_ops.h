@@ -173,14 +173,17 @@ hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st);
 constexpr int kOrthoTogether = 32;  // matrices of one launch at most
 constexpr int kOrthoSteps = 16;
 constexpr int64_t kMaxOrthoSide = int64_t(1) << 15;
+constexpr int kOrthoNarrow = 64;  // a side of at most this takes its steps in fp64
 
 // Where a matrix's pieces lie in its part of the workspace (byte offsets), n x
 // m its sides, the shorter first, padded to whole tiles; [0] high parts, [1]
 // low parts.
 struct OrthoLayout {
   int64_t n, m;
-  int parts, tile, together;  // together: matrices of one launch
-  size_t x[2], xt[2][2], a[2], b[2], rest, sums;  // xt: of even and odd steps
+  int parts, together;  // together: matrices of one launch
+  int tile_a, tile_b, tile_x;  // of the three products of a step
+  int splits, split_steps;    // of the sums of X X^T
+  size_t x[2][2], a[2], b[2], rest, sums, partials;  // x: of even and odd steps
   size_t per_matrix, total;
 };
 OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtype);
@@ -192,13 +195,14 @@ struct OrthoArgs {
   int out_dtype, steps;
   double eps;
   float scale;
-  float coefficients[3 * kOrthoSteps];
+  double coefficients[3 * kOrthoSteps];
   char* ws;
 };
 struct OrthoStep {
   float a, b, c;
-  int from;  // the transpose to read; the other one is written
-  int last;
+  int from;  // the X to read; the other one is written
+  uint32_t tiles, blocks;  // of a matrix: tiles, and workgroups
+  int parts, part_steps;
 };
 struct OrthoCall {
   OrthoArgs args;  // without x and out
@@ -207,6 +211,8 @@ struct OrthoCall {
   void* const* out;
 };
 hipError_t launch_ortho(int dtype, const OrthoCall& call, hipStream_t st);
+OrthoLayout ortho_narrow_layout(int64_t count, int64_t rows, int64_t cols);
+hipError_t launch_ortho_narrow(int dtype, const OrthoArgs& a, const OrthoLayout& l, int count, hipStream_t st);
 
 // ---------------------------------------------------------------- 8-bit activations
 

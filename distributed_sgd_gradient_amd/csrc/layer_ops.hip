@@ -558,6 +558,7 @@ int check_bias(int64_t heads, int64_t batch, int64_t queries, int64_t keys, int6
   if (keys < 1 || keys >= kMaxDim) return fail(ADASUM_EINVAL, "keys must be in [1, 2^31)");
   if (batch * heads >= kMaxDim || batch * heads * queries >= kMaxDim)
     return fail(ADASUM_EINVAL, "relative bias: the number of rows must be below 2^31");
+  if (queries + keys > kMaxReach) return fail(ADASUM_EINVAL, "queries and keys must be at most 2^30 together");
   if (offset <= -kMaxDim || offset >= kMaxDim) return fail(ADASUM_EINVAL, "offset must be within 2^31");
   if (buckets < (bidirectional ? 4 : 2) || buckets > kMaxBuckets || (bidirectional && buckets % 2 != 0))
     return fail(ADASUM_EINVAL, "buckets must be in [2, 256], in both directions even and at least 4");
@@ -781,7 +782,7 @@ int orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t col
   a.steps = steps;
   a.eps = eps;
   a.scale = (float)scale;
-  for (int i = 0; i < 3 * steps; ++i) a.coefficients[i] = (float)coefficients[i];
+  for (int i = 0; i < 3 * steps; ++i) a.coefficients[i] = coefficients[i];
   a.ws = static_cast<char*>(workspace);
   call.count = count;
   call.x = x;

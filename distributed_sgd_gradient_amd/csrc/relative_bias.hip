@@ -31,7 +31,7 @@ using namespace elem;
 
 constexpr int kTileRows = 16, kTileCols = 1024;  // of the forward pass
 constexpr int kPieces = 4;                       // pieces a lane has in flight
-constexpr int kGradUnit = 64, kGradAhead = 8;    // rows of a unit, rows in flight
+constexpr int kGradUnit = 16, kGradAhead = 8;   // rows of a unit, rows in flight
 
 // The bucket of distance n on its side: the last border at or below n.
 __device__ __forceinline__ int bucket_of(const BiasBuckets& k, uint32_t n) {
@@ -108,62 +108,71 @@ __global__ __launch_bounds__(256) void bias_kernel(BiasArgs a, BiasLayout l) {
 }
 
 // Sums along diagonals.  Diagonal D = j - i + queries - 1; LPD lanes own VEC
-// diagonals each, and a wave's 64 / LPD groups, like the four waves, take units
-// of kGradUnit rows of a sequence in turn.
+// diagonals each, and the workgroup's groups of lanes take units of kGradUnit
+// rows of a sequence in turn.
 template <typename T, int LPD>
 __global__ __launch_bounds__(256) void bias_grad_kernel(BiasGradArgs a, BiasGradLayout l) {
   constexpr int VEC = Type<T>::kVec, GROUPS = 256 / LPD;
   const int lane = threadIdx.x & (LPD - 1), group = threadIdx.x / LPD;
   uint32_t block = blockIdx.x;
-  const int64_t tile = block % l.tiles;
+  const uint32_t tile = block % l.tiles;
   block /= l.tiles;
-  const int64_t head = block % a.heads, split = block / a.heads;
-  const int64_t diagonals = a.queries + a.keys - 1;
-  const int64_t d0 = (tile * LPD + lane) * VEC;
-  const int64_t shift = d0 - (a.queries - 1);  // column of the lane's first diagonal in row 0
+  const uint32_t head = block % (uint32_t)a.heads, split = block / (uint32_t)a.heads;
+  const int queries = (int)a.queries, keys = (int)a.keys;  // together at most 2^30
+  const int tile_shift = (int)(tile * LPD * VEC) - (queries - 1);
+  const int shift = tile_shift + lane * VEC;  // column of the lane's first diagonal in row 0
   const T* base = static_cast<const T*>(a.dscores);
-  const int64_t all_rows = a.batch * a.heads * a.queries;
-  const int64_t extent = (all_rows - 1) * a.stride + a.keys;  // elements from the first to the last
-  const int64_t row_units = (a.queries + kGradUnit - 1) / kGradUnit, units = a.batch * row_units;
+  const int64_t all_rows = a.batch * a.heads * queries;
+  const uint32_t row_units = (uint32_t)(queries + kGradUnit - 1) / kGradUnit, units = (uint32_t)a.batch * row_units;
+  // A vector that reaches over its row's ends reads its neighbours in memory,
+  // whose values are dropped.  There are none before the first row and behind
+  // the last, which are taken value by value, like rows narrower than a vector.
+  const bool narrow = keys < VEC;
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-  const int64_t last_start = extent - VEC;  // where a vector may start at most; below 0: none may
-  for (int64_t unit = split * GROUPS + group; unit < units; unit += (int64_t)l.splits * GROUPS) {
-    const int64_t n = unit / row_units, begin = (unit - n * row_units) * kGradUnit;
-    const int64_t end = min(a.queries, begin + kGradUnit);
+  for (uint32_t unit = split * GROUPS + group; unit < units; unit += (uint32_t)l.splits * GROUPS) {
+    const uint32_t n = unit / row_units;
+    const int begin = (int)(unit - n * row_units) * kGradUnit, end = min(queries, begin + kGradUnit);
     // rows in which any of the tile's diagonals has a column
-    const int64_t tile_shift = tile * LPD * VEC - (a.queries - 1);
-    const int64_t lo = max(begin, -(tile_shift + LPD * VEC - 1)), hi = min(end, a.keys - tile_shift);
-    const int64_t row0 = (n * a.heads + head) * a.queries;
-    for (int64_t i0 = lo; i0 < hi; i0 += kGradAhead) {
+    int lo = max(begin, -(tile_shift + LPD * VEC - 1)), hi = min(end, keys - tile_shift);
+    const int64_t row0 = ((int64_t)n * a.heads + head) * queries;
+    auto one_row = [&](int i) {
+      const T* p = base + (row0 + i) * a.stride;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if ((uint32_t)(shift + i + e) < (uint32_t)keys) acc[e] += (float)p[shift + i + e];
+    };
+    if (lo >= hi) continue;
+    if (narrow) {
+      for (int i = lo; i < hi; ++i) one_row(i);
+      continue;
+    }
+    if (row0 + lo == 0) one_row(lo++);
+    if (lo < hi && row0 + hi == all_rows) one_row(--hi);
+    for (int i0 = lo; i0 < hi; i0 += kGradAhead) {
       v4u raw[kGradAhead];
+      const T* p = base + (row0 + i0) * a.stride;
 #pragma unroll
       for (int u = 0; u < kGradAhead; ++u) {
-        // A vector that reaches over its row's ends reads its neighbours in
-        // memory, whose values are dropped below; one that lies outside its
-        // row, or would leave the matrix, reads the row's own first (or the
-        // last possible) vector.  No branch: all loads are on their way at once.
-        const int64_t i = i0 + u, j = shift + i;
-        const int64_t start = (row0 + min(i, hi - 1)) * a.stride;
-        int64_t at = start + j;
-        if (i >= hi || j <= -VEC || j >= a.keys) at = start;
-        at = max<int64_t>(0, min(at, last_start));
-        raw[u] = last_start >= 0 ? load_at<v4u, sizeof(T)>(base + at) : v4u{0u, 0u, 0u, 0u};
+        // no branch: all loads are on their way at once.  A lane without a
+        // column in this row reads the row's first vector.
+        const int j = shift + i0 + u;
+        const int64_t row = i0 + u < hi ? u * a.stride : 0;
+        const bool inside = (uint32_t)(j + VEC - 1) < (uint32_t)(keys + VEC - 1) && i0 + u < hi;
+        raw[u] = load_at<v4u, sizeof(T)>(p + row + (inside ? j : 0));
       }
 #pragma unroll
       for (int u = 0; u < kGradAhead; ++u) {
-        const int64_t i = i0 + u, j = shift + i, at = (row0 + i) * a.stride + j;
-        const bool there = i < hi && at >= 0 && at <= last_start;
+        const int j = shift + i0 + u;
         float v[VEC];
         widen<T>(raw[u], v);
+        if (!((uint32_t)j <= (uint32_t)(keys - VEC) && i0 + u < hi)) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += there && j + e >= 0 && j + e < a.keys ? v[e] : 0.f;
-        if (i < hi && !there) {  // the matrix's first and last row
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (j + e >= 0 && j + e < a.keys) acc[e] += (float)base[at + e];
+          for (int e = 0; e < VEC; ++e) v[e] = (uint32_t)(j + e) < (uint32_t)keys && i0 + u < hi ? v[e] : 0.f;
         }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += v[e];
       }
     }
   }
@@ -173,7 +182,8 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(BiasGradArgs a, BiasGrad
   for (int e = 0; e < VEC; ++e) part[e * 256 + threadIdx.x] = acc[e];
   __syncthreads();
   if (group == 0) {
-    float* out = a.partials + (split * a.heads + head) * diagonals;
+    const int diagonals = queries + keys - 1, d0 = (int)(tile * LPD + lane) * VEC;
+    float* out = a.partials + ((int64_t)split * a.heads + head) * diagonals;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       float s = 0.f;
@@ -185,7 +195,7 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(BiasGradArgs a, BiasGrad
 }
 
 // dtable[b][h]: bucket b's diagonals of every split, summed in fp64 by a
-// workgroup in a fixed order.
+// workgroup in a fixed order: 64 diagonals and four splits at a time.
 __global__ __launch_bounds__(256) void bias_join_kernel(BiasGradArgs a, int splits) {
   __shared__ double sums[256];
   const int64_t head = blockIdx.x % (uint32_t)a.heads;
@@ -206,13 +216,16 @@ __global__ __launch_bounds__(256) void bias_join_kernel(BiasGradArgs a, int spli
   const int64_t diagonals = a.queries + a.keys - 1, zero = a.queries - 1 + a.offset;
   lo = max<int64_t>(lo + zero, 0);
   hi = min(hi + zero, diagonals - 1);
-  const int64_t width = hi - lo + 1;
+  const int64_t pitch = a.heads * diagonals;
   double t = 0.0;
-  if (width > 0) {
-    const int64_t count = width * splits;
-    for (int64_t p = threadIdx.x; p < count; p += 256) {
-      const int64_t q = p / width;
-      t += (double)a.partials[(q * a.heads + head) * diagonals + lo + (p - q * width)];
+  for (int64_t d = lo + (threadIdx.x & 63); d <= hi; d += 64) {
+    const float* p = a.partials + head * diagonals + d;
+    for (int first = threadIdx.x >> 6; first < splits; first += 32) {
+      float v[8];  // splits past the last are read at the last: eight loads at once
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = p[min(first + 4 * u, splits - 1) * pitch];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) t += first + 4 * u < splits ? (double)v[u] : 0.0;
     }
   }
   sums[threadIdx.x] = t;
@@ -308,10 +321,10 @@ BiasGradLayout bias_grad_layout(int64_t batch, int64_t heads, int64_t queries, i
   l.lanes = diagonals <= 32 * vec ? 16 : 64;
   l.tiles = ceil_div(diagonals, l.lanes * vec);
   const int64_t units = batch * ceil_div(queries, kGradUnit), groups = 256 / l.lanes;
-  // as many workgroups as fill the card twice, each group with a unit at least;
-  // and no more than 64 units, 4096 rows, in one fp32 sum
-  const int64_t fill = ceil_div(2 * 4 * kCUs, l.tiles * heads), most = ceil_div(units, groups);
-  l.splits = std::max<int64_t>({1, std::min(fill, most), ceil_div(units, groups * 64)});
+  // four workgroups a CU, each group with a unit at least; and no more than 4096
+  // rows in one fp32 sum
+  const int64_t fill = ceil_div(4 * kCUs, l.tiles * heads), most = ceil_div(units, groups);
+  l.splits = std::max<int64_t>({1, std::min(fill, most), ceil_div(units, groups * (4096 / kGradUnit))});
   l.blocks = l.splits * heads * l.tiles;
   l.bytes = (size_t)l.splits * heads * diagonals * sizeof(float);
   return l;

@@ -340,3 +340,20 @@ __forceinline__ void on_cpu_load_lds(G from, L to) {
 #define __builtin_amdgcn_global_load_lds(from, to, bytes, offset, aux) on_cpu_load_lds(from, to)
 #define __builtin_amdgcn_s_waitcnt(counts) ((void)0)
 #define __builtin_amdgcn_s_barrier() on_cpu::wait(on_cpu::kBarrier)
+
+// A lane of a 16 x 16 x 4 product in fp64 holds term l / 16 of row or column
+// l % 16, and of the sums rows 4 r + l / 16 of column l % 16.
+template <typename C>
+__forceinline__ C on_cpu_multiply64(double a, double b, C c) {
+  struct Both {
+    double a, b;
+  } mine{a, b};
+  return on_cpu::together(mine, [&](auto from) {
+    const unsigned l = on_cpu::lane_id();
+    C r = c;
+    for (unsigned q = 0; q < 4; ++q)
+      for (unsigned k = 0; k < 4; ++k) r[q] += from(k * 16 + 4 * q + l / 16).a * from(k * 16 + l % 16).b;
+    return r;
+  });
+}
+#define __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, x, y, z) on_cpu_multiply64(a, b, c)

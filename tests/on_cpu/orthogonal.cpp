@@ -1,6 +1,7 @@
 // The orthogonal update's kernels on the CPU: count rows cols dtype out_dtype
 // steps.
 #include "orthogonal.inc"
+#include "orthogonal_narrow.inc"
 #include "values.h"
 
 using namespace adasum;
@@ -29,7 +30,7 @@ int main(int, char** arg) {
   call.args.steps = steps;
   call.args.eps = 1e-7;
   call.args.scale = 1.5f;
-  const float k[3] = {3.4445f, -4.775f, 2.0315f};
+  const double k[3] = {3.4445, -4.775, 2.0315};
   for (int i = 0; i < 3 * steps; ++i) call.args.coefficients[i] = k[i % 3];
   call.args.ws = on_cpu::guarded(l.total);
   call.count = count;

@@ -3,7 +3,16 @@ on the CPU, from their own sources (see test_kernels_on_cpu.py)."""
 
 import pytest
 
-from test_kernels_on_cpu import BF16, F16, F32, program, pytestmark, run  # noqa: F401
+from test_kernels_on_cpu import BF16, F16, F32, as_cpp, program, pytestmark, run  # noqa: F401
+
+
+@pytest.fixture(scope="module")
+def orthogonal(program, tmp_path_factory):  # noqa: F811
+    """The program of both sources of the orthogonal updates."""
+    work = tmp_path_factory.getbasetemp()
+    for folder in work.glob("on_cpu*"):
+        (folder / "orthogonal_narrow.inc").write_text(as_cpp("orthogonal_narrow.hip"))
+    return program("orthogonal")
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
@@ -34,9 +43,12 @@ def test_relative_bias(program, batch, heads, queries, keys, offset, buckets, re
 @pytest.mark.parametrize("count,rows,cols,dtype,out_dtype,steps", [
     (1, 1, 1, F32, F32, 5),
     (2, 5, 9, BF16, BF16, 5),
-    (1, 30, 130, F16, F16, 3),
+    (1, 30, 130, F16, F16, 5),
+    (2, 200, 64, F32, F16, 4),
+    (1, 65, 66, F32, F32, 5),
     (1, 140, 20, F32, F32, 2),
     (1, 140, 131, F32, BF16, 1),
+    (1, 258, 260, BF16, BF16, 1),
 ])
-def test_orthogonal(program, count, rows, cols, dtype, out_dtype, steps):  # noqa: F811
-    run(program("orthogonal"), count, rows, cols, dtype, out_dtype, steps)
+def test_orthogonal(orthogonal, count, rows, cols, dtype, out_dtype, steps):
+    run(orthogonal, count, rows, cols, dtype, out_dtype, steps)
