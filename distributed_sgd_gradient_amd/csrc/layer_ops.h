@@ -171,6 +171,7 @@ hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st);
 // ---------------------------------------------------------------- orthogonal updates
 
 constexpr int kOrthoTogether = 32;  // matrices of one launch at most
+constexpr size_t kOrthoWorkspace = size_t(4) << 30;  // and no more than this takes, if it is two or more
 constexpr int kOrthoSteps = 16;
 constexpr int64_t kMaxOrthoSide = int64_t(1) << 15;
 constexpr int kOrthoNarrow = 64;  // a side of at most this takes its steps in fp64

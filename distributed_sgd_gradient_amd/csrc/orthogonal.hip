@@ -476,6 +476,16 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
     return;
   }
   if constexpr (kBase && !kEarly) read_base(0, 0);
+  // Where LDS holds the tile, it goes there first and leaves in whole rows.  Every
+  // wave is past its reads: the last barrier of the loop lies behind them.
+  constexpr int kStored = PARTS == 2 || APPLY ? 2 : 1;
+  constexpr bool kStash = KIND != kLastB && kStored * T * T * 2 <= (int)sizeof(lds);
+  v4u* const stash = &lds[0][0][0];
+  // 16-byte pieces permuted within a row, so that 16 lanes' rows, MP apart, find
+  // different banks
+  auto stash_at = [](int row, int piece) __attribute__((always_inline)) {
+    return row * (T / 8) + (piece ^ (row / MP & (T / 8 - 1)));
+  };
   const bool turn = KIND == kLastB ? a.rows > a.cols : tp != tq;
   v8h hi[MP], lo[MP];
   float v[MP][8];
@@ -513,9 +523,15 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
         hi[i][e] = h;
         lo[i][e] = t;
       }
-      const int64_t at_out = ((p + i) * width + q + 32 * j) * 2;
-      *reinterpret_cast<v8h*>(to[0] + at_out) = hi[i];
-      if (PARTS == 2 || APPLY) *reinterpret_cast<v8h*>(to[1] + at_out) = lo[i];
+      if constexpr (kStash) {
+        const int place = stash_at((int)(p - p0) + i, (int)(q - q0) / 8 + 4 * j);
+        stash[place] = __builtin_bit_cast(v4u, hi[i]);
+        if constexpr (kStored == 2) stash[T * T / 8 + place] = __builtin_bit_cast(v4u, lo[i]);
+      } else {
+        const int64_t at_out = ((p + i) * width + q + 32 * j) * 2;
+        *reinterpret_cast<v8h*>(to[0] + at_out) = hi[i];
+        if constexpr (kStored == 2) *reinterpret_cast<v8h*>(to[1] + at_out) = lo[i];
+      }
     }
     if (g % (MP / kGroup) != MP / kGroup - 1) continue;
     // all MP rows of these columns are there
@@ -551,6 +567,18 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
           *reinterpret_cast<Column*>(to[h] + ((q + 32 * j + e) * l.n + p) * 2) = t;
         }
     }
+  }
+  if constexpr (kStash) {
+    __syncthreads();
+    constexpr int kThreads = kWaves * 64, kRow = T / 8;
+#pragma unroll
+    for (int h = 0; h < kStored; ++h)
+#pragma unroll
+      for (int u = 0; u < T * kRow / kThreads; ++u) {
+        const int place = u * kThreads + tid, row = place / kRow, piece = place % kRow;
+        *reinterpret_cast<v4u*>(to[h] + ((p0 + row) * width + q0 + piece * 8) * 2) =
+            stash[h * T * kRow + stash_at(row, piece)];
+      }
   }
 }
 
@@ -668,12 +696,12 @@ double cost_of(bool x, int parts, int index, int64_t blocks, int64_t steps) {
 
 }  // namespace
 
-OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
-  const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
-  if (n <= kOrthoNarrow) return ortho_narrow_layout(count, rows, cols);
+namespace {
+
+OrthoLayout layout_of(int64_t n, int64_t m, int parts, int together) {
   OrthoLayout l{};
-  l.parts = out_dtype == 2 && n > kOnePartSide ? 1 : 2;
-  l.together = (int)std::min<int64_t>(count, kOrthoTogether);
+  l.parts = parts;
+  l.together = together;
   // the tiles of the three products, and the parts of A's sums, that take the
   // least time; all sides are padded to the largest tile
   double best = 1e30;
@@ -710,15 +738,6 @@ OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtyp
       l.splits = splits;
     }
   }
-#ifdef TILES
-  {
-    const int t[4] = {TILES};
-    const int64_t pad = std::max(t[0], std::max(t[1], t[2]));
-    l.tile_a = t[0], l.tile_b = t[1], l.tile_x = t[2], l.splits = t[3];
-    l.n = ceil_div(n, pad) * pad;
-    l.m = ceil_div(m, pad) * pad;
-  }
-#endif
   const int64_t steps = l.m / kStep;
   l.split_steps = (int)ceil_div(steps, l.splits);
   l.splits = (int)ceil_div(steps, l.split_steps);
@@ -743,6 +762,17 @@ OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtyp
   l.per_matrix = at;
   l.total = at * l.together;
   return l;
+}
+
+}  // namespace
+
+OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
+  const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
+  if (n <= kOrthoNarrow) return ortho_narrow_layout(count, rows, cols);
+  const int parts = out_dtype == 2 && n > kOnePartSide ? 1 : 2;
+  const OrthoLayout l = layout_of(n, m, parts, (int)std::min<int64_t>(count, kOrthoTogether));
+  if (l.total <= kOrthoWorkspace) return l;
+  return layout_of(n, m, parts, (int)std::max<size_t>(1, kOrthoWorkspace / l.per_matrix));
 }
 
 hipError_t launch_ortho(int dtype, const OrthoCall& call, hipStream_t st) {

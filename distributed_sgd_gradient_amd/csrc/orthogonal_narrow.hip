@@ -133,18 +133,25 @@ __global__ __launch_bounds__(kThreads) void narrow_steps_kernel(OrthoArgs a, Ort
   const int n = (int)min(a.rows, a.cols), blocks = (n + 15) / 16, side = blocks * 16;
   const int wave = threadIdx.x >> 6, tiles = blocks * (blocks + 1) / 2;
   double *g = space[0], *p = space[1], *q = space[2], *t = space[3];
-  for (int e = threadIdx.x; e < side * side; e += kThreads) {
-    const int i = e / side, j = e % side;
-    const double* from = parts + i * kSide + j;
-    double s = 0.0;
-    for (int first = 0; first < l.splits; first += 8) {
-      double v[8];  // parts past the last are read at the last: eight loads at once
+  constexpr int kOwn = (kSide * kSide + kThreads - 1) / kThreads;  // of a lane
+  double sum[kOwn] = {};
+  for (int first = 0; first < l.splits; first += 4) {
+    double v[kOwn][4];  // parts past the last are read at the last: all loads at once
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = from[(int64_t)min(first + u, l.splits - 1) * kSide * kSide];
+    for (int u = 0; u < kOwn; ++u)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s += first + u < l.splits ? v[u] : 0.0;
-    }
-    g[i * kPitch + j] = s;
+      for (int k = 0; k < 4; ++k)
+        v[u][k] = parts[(int64_t)min(first + k, l.splits - 1) * kSide * kSide +
+                        min((int)threadIdx.x + u * kThreads, kSide * kSide - 1)];
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sum[u] += first + k < l.splits ? v[u][k] : 0.0;
+  }
+#pragma unroll
+  for (int u = 0; u < kOwn; ++u) {
+    const int e = threadIdx.x + u * kThreads;
+    if (e < kSide * kSide) g[e / kSide * kPitch + e % kSide] = sum[u];
   }
   __syncthreads();
   double squares = 0.0;

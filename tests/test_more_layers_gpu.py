@@ -488,17 +488,52 @@ def test_orthogonalize_special_matrices(gpu):
         assert torch.equal(A.orthogonalize(x * 2.0 ** 100, dtype=out), A.orthogonalize(x * 2.0 ** 90, dtype=out))
         t = A.orthogonalize(x.transpose(1, 2).contiguous(), dtype=out)
         check_orthogonal(t.transpose(1, 2), plain_orthogonal(x), out, 90)
+    # the narrow path
+    x = spectrum(452, 20, 90, F32, count=5)
+    for steps, k in ((5, K), (1, (1.5, -0.5, 0.0))):
+        want = A.orthogonalize(x, steps=steps, coefficients=k)
+        y = x.clone()
+        y[1] = 0
+        y[2, 3, 4] = float("nan")
+        y[3, 19, 89] = float("inf")
+        got = A.orthogonalize(y, steps=steps, coefficients=k)
+        assert same(got[[0, 4]], want[[0, 4]]) and not bool(got[1].any()) and bool(got[2:4].isnan().all())
     # eps counts where the update is as small
     x = spectrum(451, 30, 40, F32) * 1e-6
     check_orthogonal(A.orthogonalize(x, eps=1e-6), plain_orthogonal(x, eps=1e-6), F32, 40)
 
 
 def test_orthogonalize_large(gpu):
-    """BERT-Large's matrices, against 64-bit products on the GPU."""
-    for (n, m), dtype in (((1024, 1024), BF16), ((4096, 1024), F32), ((1024, 4096), BF16)):
-        flush_print(f"orthogonalize {n}x{m} {dtype}")
-        x = spectrum(460, n, m, dtype, "strong")
-        check_orthogonal(A.orthogonalize(x), plain_orthogonal(x), dtype, 4096)
+    """BERT-Large's matrices, one and as many as fill the card, against 64-bit
+    products on the GPU: every tile that the kernels take."""
+    for count, (n, m), dtype in ((1, (1024, 1024), BF16), (1, (4096, 1024), F32), (1, (1024, 4096), BF16),
+                                 (24, (1024, 1024), BF16), (9, (1024, 1024), BF16), (8, (4096, 1024), BF16),
+                                 (16, (1024, 1024), F16), (6, (4000, 1000), F32), (20, (300, 500), BF16),
+                                 (33, (700, 260), BF16), (40, (64, 64), BF16), (33, (3, 2000), F32)):
+        flush_print(f"orthogonalize {count}x{n}x{m} {dtype}")
+        x = spectrum(460, n, m, dtype, "strong" if min(n, m) > 3 else "normal", count)
+        got = A.orthogonalize(x)
+        for i in {0, count // 2, count - 1}:
+            check_orthogonal(got[i], plain_orthogonal(x[i]), dtype, max(n, m))
+        if count > 1:  # bitwise the same for the same matrix
+            x[0] = x[count - 1]
+            got = A.orthogonalize(x)
+            assert torch.equal(got[0], got[count - 1])
+
+
+def test_orthogonalize_two_at_once(gpu):
+    """Two calls on two streams, each with a workspace of its own."""
+    x, y = spectrum(470, 300, 400, BF16, count=5), spectrum(471, 50, 900, F32, count=3)
+    want = A.orthogonalize(x), A.orthogonalize(y)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (one, two):
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        a = A.orthogonalize(x, stream=one)
+        b = A.orthogonalize(y, stream=two)
+        c = A.orthogonalize(x, stream=two)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(c, want[0])
 
 
 # ---------------------------------------------------------------- together

@@ -219,6 +219,11 @@ def test_workspace_sizes():
     one = lib.adasum_orthogonalize_workspace_bytes(1, 1000, 600, F32)
     assert one >= 2 * (4 * 1000 * 600 + 2 * 600 * 600)
     assert lib.adasum_orthogonalize_workspace_bytes(1, 600, 1000, F32) == one
+    # the widest: 16 bytes of X's parts and, in two parts, 8 of A and 8 of B for each element; one at a time
+    side = 1 << 15
+    most = lib.adasum_orthogonalize_workspace_bytes(1 << 16, side, side, F32)
+    assert 16 * side * side <= most <= 20 * side * side
+    assert lib.adasum_orthogonalize_workspace_bytes(1 << 16, 4096, 4096, BF16) <= 4 << 30
     # matrices of one call take turns
     assert lib.adasum_orthogonalize_workspace_bytes(1 << 16, 1000, 600, F32) <= 64 * one
     assert lib.adasum_orthogonalize_workspace_bytes(1, 30, 1 << 16, F32) == _native.EINVAL
