@@ -4,8 +4,15 @@
 //
 //   A = X X^T,  B = b A + c A A,  X <- a X + B X      steps times
 //
-// which takes every singular value s to a s + b s^3 + c s^5.  Bound by the
-// matrix cores.
+// which takes every singular value s to a s + b s^3 + c s^5.
+//
+// Bound by the matrix cores, the card's power, and X's traffic: 24 matrices of
+// 1024 x 1024 in bf16 take 840 to 860 us, 600 TFLOP/s with half of the symmetric
+// products (a library product of 8192^3 in fp16 reaches 1127).  A step there is 41
+// us of A, 42 of B and 96 of X; the loops alone, whose matrix instructions run at
+// 1.1 PFLOP/s, take 27, 25 and 70, the rest is the writing of the results, which
+// begins when all workgroups end.  Matrices with a side of at most 64 are in
+// orthogonal_narrow.hip.
 //
 // Products take fp16 operands and sum in fp32.  X is kept as hi + lo, two fp16
 // of 22 bits together, and a X is added in fp32 from both: rounding X itself to
@@ -227,7 +234,8 @@ __device__ __forceinline__ void meet() {
 
 // Rows along the sum, of 64 values, in 16-byte pieces permuted within a row.
 // The LDS serves lanes 0-3, 12-15 and 20-27 of a 16-byte read together, and the
-// other 16 of each 32: with these keys each set finds different banks.
+// other 16 of each 32: with these keys each set finds different banks (no
+// conflicts counted; where rows 0-3 and 4-7 met, every read took twice as long).
 __device__ __forceinline__ int along_key(int row) { return (row >> 1) & 7; }
 // Rows across the sum, of T values, in segments of 32 permuted within a row: a
 // transposing read takes half of the same segment of 16 rows.
@@ -239,8 +247,10 @@ __device__ __forceinline__ int across_key(int row) {
 // A tile of T x T of C = P Q, summed over kStep values at a time; P's rows lie
 // along the sum, and Q's columns (kGramX, kSquareA: C = P Q^T, rows of one
 // symmetric matrix) or, of a product with X, Q's rows across it, which transposing
-// reads turn.  Loads go straight to LDS, kStages steps ahead, and LDS is
-// read one step ahead of the products.
+// reads turn.  Loads go straight to LDS, kStages steps ahead, and LDS is read half
+// a step ahead of the products.  Rows of 128 bytes, not of 64 (24 x 1024 x 1024
+// bf16: A 39 us against 45, X 110 against 121); tiles of X written from the
+// registers, 64 bytes a row, not through LDS: X 100 us against 96.
 template <int KIND, int PARTS, int T>
 __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(OrthoArgs a, OrthoLayout l, OrthoStep step) {
   using S = Tile<T, PARTS>;
@@ -673,25 +683,30 @@ hipError_t steps_of(const OrthoArgs& a, const OrthoLayout& l, int count, hipStre
   return hipSuccess;
 }
 
-// What a product takes, in us: `steps` of 64 of the sum in each of `blocks`
-// workgroups, of which `slots` run at once.
+// What a product takes, in us: a round of `slots` workgroups at once starts and
+// ends (fixed) and takes `steps` of 64 of the sum, each of `full` where the card
+// is full, down to `alone` where it is nearly empty.  From measured products of 1
+// to 24 matrices of 1024 x 1024 and 1 of 1024 x 4096 and 4096 x 4096.  Of 36 calls
+// from 100 x 100 to 4096 x 4096, 1 to 24 matrices, 31 take at most 5 % longer than
+// with the best of six fixed choices, the others up to 14 % (24 x 1024 x 1024 bf16:
+// 854 us, with tiles of 64 alone 1322, of 128 alone 891; 1 x 1024 x 1024: 151, 152
+// and 271).
 struct Cost {
   int slots;
-  double alone, full, fixed;  // a step on a card half empty, and on a full one; a workgroup's start and end
+  double alone, full, fixed;
 };
-constexpr Cost kCosts[2][2][3] = {  // X's products or A's and B's; parts; tiles of 64, 128, 256
-    {{{512, 0.25, 0.45, 4}, {512, 0.72, 1.3, 5}, {256, 1.6, 1.75, 12}},
-     {{512, 0.68, 1.3, 4}, {256, 1.3, 1.6, 4}, {256, 1e9, 1e9, 0}}},
-    {{{512, 0.66, 0.75, 4}, {512, 1.1, 1.6, 8}, {256, 2.4, 2.5, 25}},
-     {{512, 1.1, 1.3, 4}, {256, 1.9, 1.95, 5}, {256, 1e9, 1e9, 0}}}};
+constexpr Cost kCosts[2][2][3] = {  // A and B, or X; one part or two; tiles of 64, 128, 256
+    {{{512, 0.28, 0.45, 3}, {512, 0.72, 1.25, 5}, {256, 1.2, 1.75, 11}},
+     {{512, 0.6, 0.95, 4}, {256, 1.3, 1.6, 4}, {256, 1e9, 1e9, 0}}},
+    {{{512, 0.6, 0.7, 4}, {512, 0.8, 1.5, 8}, {256, 1.1, 2.4, 25}},
+     {{512, 1.0, 1.35, 4}, {256, 1.5, 1.9, 5}, {256, 1e9, 1e9, 0}}}};
 
 double cost_of(bool x, int parts, int index, int64_t blocks, int64_t steps) {
   const Cost& c = kCosts[x][parts - 1][index];
-  if (2 * blocks <= c.slots) return c.fixed + steps * c.alone;
-  // one workgroup a CU: whole rounds; two: they take turns
-  const double rounds = c.slots == kCUs ? (double)ceil_div(blocks, c.slots)
-                                        : std::max(1.0, (double)blocks / c.slots);
-  return rounds * (c.fixed + steps * c.full);
+  const int64_t rounds = blocks / c.slots;
+  const double rest = (double)(blocks - rounds * c.slots) / c.slots;
+  return rounds * (c.fixed + steps * c.full) +
+         (rest > 0 ? c.fixed + steps * (c.alone + (c.full - c.alone) * rest) : 0.0);
 }
 
 }  // namespace
@@ -717,7 +732,7 @@ OrthoLayout layout_of(int64_t n, int64_t m, int parts, int together) {
         const int64_t steps = (kind == 0 ? pm : pn) / kStep;
         for (int64_t s = 1; s <= (kind == 0 ? std::min<int64_t>(16, steps / 4) : 1) || s == 1; ++s) {
           // the parts are written, read, and waited for
-          const double join = s == 1 ? 0 : 4 + 8e-6 * (double)(s * pn * pn * l.together) / 4;
+          const double join = s == 1 ? 0 : 8 + 6e-7 * (double)(s * pn * pn * l.together);
           const double c = cost_of(kind == 2, l.parts, i, tiles * s, ceil_div(steps, s)) + join;
           if (c < least) {
             least = c;
