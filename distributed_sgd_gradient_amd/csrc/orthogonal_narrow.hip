@@ -10,8 +10,12 @@
 // G holds the squares of the singular values, so everything is in fp64, where
 // those that fp32 can tell from zero keep their digits.  Three launches instead
 // of three a step: partial sums of G over the long side, the steps in one
-// workgroup a matrix on the fp64 matrix cores, and the product with X0.  Bound by
-// the latency of the steps: 17 products of 64 x 64 one after another.
+// workgroup a matrix on the fp64 matrix cores, a wave for each tile of 16 x 16 on
+// and above the diagonal, and the product with X0.  Bound by the latency of the
+// steps, in which three products follow one another: 61 x 769 fp32 in 5 steps
+// takes 8 + 39 + 11 us (the steps with a product's sum in one chain of matrix
+// instructions, and LDS read between them: 48; with fp32 steps through the
+// products of orthogonal.hip: 254 a call against 59).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -30,9 +34,6 @@ typedef double v4d __attribute__((ext_vector_type(4)));
 
 constexpr int kSide = kOrthoNarrow, kChunk = 64;  // columns of X at a time
 constexpr int kPitch = kSide + 2;                 // of a matrix in LDS, in doubles
-constexpr int kThreads = 640, kWaves = kThreads / 64;  // a wave for each tile on or above the diagonal
-constexpr int kTilesOfWave = 1;
-static_assert(kTilesOfWave * kWaves >= 10, "all tiles of 64 x 64");
 
 // 64 columns from k0 on of X (the shorter side being its rows) as tile[k][i];
 // zeros outside.  All of a lane's loads are on their way before the first is
@@ -90,59 +91,55 @@ __global__ __launch_bounds__(256) void narrow_gram_kernel(OrthoArgs a, OrthoLayo
     for (int f = 0; f < 4; ++f) out[(i0 + e) * kSide + j0 + f] = acc[e][f];
 }
 
-// A tile of 16 x 16 of A B, of symmetric matrices that commute, `side` wide:
-// tile t of those on and above the diagonal, row by row.
-struct Place {
-  int i, j;  // of the tile
-};
-__device__ __forceinline__ Place place_of(int t, int blocks) {
-  int i = 0;
-  while (t >= blocks - i) {
-    t -= blocks - i;
-    ++i;
-  }
-  return {i * 16, (i + t) * 16};
-}
-__device__ __forceinline__ v4d tile_product(const double* a, const double* b, Place at, int side) {
+// The steps of a matrix whose narrow side is B blocks of 16: a wave for each of
+// the tiles of 16 x 16 on and above the diagonal.
+template <int B>
+constexpr int tiles_of = B * (B + 1) / 2;
+
+// The wave's tile of U V, of symmetric matrices that commute.
+template <int B>
+__device__ __forceinline__ v4d tile_product(const double* u, const double* v, int ti, int tj) {
   const int lane = threadIdx.x & 63;
-  const double* u = a + (at.i + (lane & 15)) * kPitch + (lane >> 4);
-  const double* v = b + (at.j + (lane & 15)) * kPitch + (lane >> 4);  // a column of B is its row
-  v4d acc[2] = {{0.0, 0.0, 0.0, 0.0}, {0.0, 0.0, 0.0, 0.0}};  // two chains, added at the end
-  for (int k = 0; k < side; k += 16)
+  const double* from_u = u + (ti + (lane & 15)) * kPitch + (lane >> 4);
+  const double* from_v = v + (tj + (lane & 15)) * kPitch + (lane >> 4);  // a column of V is its row
+  double x[4 * B], y[4 * B];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      acc[e & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(u[k + 4 * e], v[k + 4 * e], acc[e & 1], 0, 0, 0);
+  for (int k = 0; k < 4 * B; ++k) {
+    x[k] = from_u[4 * k];
+    y[k] = from_v[4 * k];
+  }
+  v4d acc[2] = {{0.0, 0.0, 0.0, 0.0}, {0.0, 0.0, 0.0, 0.0}};  // two chains, added at the end
+#pragma unroll
+  for (int k = 0; k < 4 * B; ++k) acc[k & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[k], y[k], acc[k & 1], 0, 0, 0);
   return acc[0] + acc[1];
 }
-// f(place in a matrix, value) for the tile's values and their mirror images.
-template <typename F>
-__device__ __forceinline__ void each_place(Place at, v4d c, F f) {
-  const int lane = threadIdx.x & 63, j = at.j + (lane & 15);
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {  // a lane: rows 4 r + lane / 16 of column lane % 16
-    const int i = at.i + 4 * r + (lane >> 4);
-    f(i, j, i * kPitch + j, c[r]);
-    if (at.i != at.j) f(j, i, j * kPitch + i, c[r]);
-  }
-}
 
-__global__ __launch_bounds__(kThreads) void narrow_steps_kernel(OrthoArgs a, OrthoLayout l) {
-  __shared__ double space[4][kSide * kPitch];
+template <int B>
+__global__ __launch_bounds__((64 * tiles_of<B>)) void narrow_steps_kernel(OrthoArgs a, OrthoLayout l) {
+  constexpr int kThreads = 64 * tiles_of<B>, kWidth = 16 * B;
+  __shared__ double space[4][kWidth * kPitch];
   char* ws = a.ws + blockIdx.x * l.per_matrix;
   const double* parts = reinterpret_cast<const double*>(ws + l.partials);
-  const int n = (int)min(a.rows, a.cols), blocks = (n + 15) / 16, side = blocks * 16;
-  const int wave = threadIdx.x >> 6, tiles = blocks * (blocks + 1) / 2;
+  const int n = (int)min(a.rows, a.cols), lane = threadIdx.x & 63;
+  int ti = 0, tj = threadIdx.x >> 6;  // the wave's tile, row by row
+  while (tj >= B - ti) {
+    tj -= B - ti;
+    ++ti;
+  }
+  tj = (tj + ti) * 16;
+  ti *= 16;
   double *g = space[0], *p = space[1], *q = space[2], *t = space[3];
-  constexpr int kOwn = (kSide * kSide + kThreads - 1) / kThreads;  // of a lane
+  constexpr int kOwn = (kWidth * kWidth + kThreads - 1) / kThreads;  // values of G of a lane
   double sum[kOwn] = {};
   for (int first = 0; first < l.splits; first += 4) {
     double v[kOwn][4];  // parts past the last are read at the last: all loads at once
 #pragma unroll
     for (int u = 0; u < kOwn; ++u)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        v[u][k] = parts[(int64_t)min(first + k, l.splits - 1) * kSide * kSide +
-                        min((int)threadIdx.x + u * kThreads, kSide * kSide - 1)];
+      for (int k = 0; k < 4; ++k) {
+        const int e = min((int)threadIdx.x + u * kThreads, kWidth * kWidth - 1);
+        v[u][k] = parts[(int64_t)min(first + k, l.splits - 1) * kSide * kSide + e / kWidth * kSide + e % kWidth];
+      }
 #pragma unroll
     for (int u = 0; u < kOwn; ++u)
 #pragma unroll
@@ -151,75 +148,62 @@ __global__ __launch_bounds__(kThreads) void narrow_steps_kernel(OrthoArgs a, Ort
 #pragma unroll
   for (int u = 0; u < kOwn; ++u) {
     const int e = threadIdx.x + u * kThreads;
-    if (e < kSide * kSide) g[e / kSide * kPitch + e % kSide] = sum[u];
+    if (e < kWidth * kWidth) g[e / kWidth * kPitch + e % kWidth] = sum[u];
   }
   __syncthreads();
-  double squares = 0.0;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) squares += g[i * kPitch + i];
+  double squares = lane < n ? g[lane * kPitch + lane] : 0.0;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) squares += __shfl_xor(squares, d);
   const double f = 1.0 / (sqrt(squares) + a.eps);
   __syncthreads();
-  for (int e = threadIdx.x; e < side * side; e += kThreads) g[e / side * kPitch + e % side] *= f * f;
+#pragma unroll
+  for (int u = 0; u < kOwn; ++u) {
+    const int e = threadIdx.x + u * kThreads;
+    if (e < kWidth * kWidth) g[e / kWidth * kPitch + e % kWidth] = sum[u] * (f * f);
+  }
   __syncthreads();
+  // A lane's places of its wave's tile: rows 4 r + lane / 16 of column lane % 16,
+  // and their mirror images.
+  const int row = ti + (lane >> 4), column = tj + (lane & 15);
+  auto put = [&](double* to, v4d v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      to[(row + 4 * r) * kPitch + column] = v[r];
+      if (ti != tj) to[column * kPitch + row + 4 * r] = v[r];
+    }
+  };
   for (int s = 0; s < a.steps; ++s) {
     const double ca = a.coefficients[3 * s], cb = a.coefficients[3 * s + 1], cc = a.coefficients[3 * s + 2];
-    for (int k = wave; k < tiles; k += kWaves) {
-      const Place at = place_of(k, blocks);
-      each_place(at, tile_product(g, g, at, side), [&](int i, int j, int where, double v) {
-        v = cb * g[where] + cc * v + (i == j ? ca : 0.0);
-        p[where] = v;
-        if (s == 0) q[where] = v;
-      });
-    }
+    v4d v = tile_product<B>(g, g, ti, tj);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      v[r] = cb * g[(row + 4 * r) * kPitch + column] + cc * v[r] + (row + 4 * r == column ? ca : 0.0);
+    put(p, v);
+    if (s == 0) put(q, v);
     __syncthreads();
-    if (s == 0) {  // Q = P; T = P G
-      if (a.steps == 1) break;
-      for (int k = wave; k < tiles; k += kWaves) {
-        const Place at = place_of(k, blocks);
-        each_place(at, tile_product(p, g, at, side), [&](int, int, int where, double v) { t[where] = v; });
-      }
-      __syncthreads();
-      for (int k = wave; k < tiles; k += kWaves) {
-        const Place at = place_of(k, blocks);
-        each_place(at, tile_product(t, p, at, side), [&](int, int, int where, double v) { g[where] = v; });
-      }
-      __syncthreads();
-      continue;
-    }
-    // T = P Q and, but for the last step, P G: each wave keeps its tiles of the
-    // latter until everyone has read G
     const bool last = s + 1 == a.steps;
-    v4d kept[kTilesOfWave];
-#pragma unroll
-    for (int u = 0; u < kTilesOfWave; ++u) {
-      const int k = wave + u * kWaves;
-      if (k < tiles) {
-        const Place at = place_of(k, blocks);
-        each_place(at, tile_product(p, q, at, side), [&](int, int, int where, double v) { t[where] = v; });
-        if (!last) kept[u] = tile_product(p, g, at, side);
-      }
+    if (s > 0) {
+      v = tile_product<B>(p, q, ti, tj);
+      put(t, v);
     }
+    if (!last) v = tile_product<B>(p, g, ti, tj);
     __syncthreads();
-    double* const free = q;
-    q = t;
-    t = free;
+    if (s > 0) {  // T is the new Q, and Q's place is free
+      double* const free = q;
+      q = t;
+      t = free;
+    }
     if (last) break;
-#pragma unroll
-    for (int u = 0; u < kTilesOfWave; ++u) {
-      const int k = wave + u * kWaves;
-      if (k < tiles) each_place(place_of(k, blocks), kept[u], [&](int, int, int where, double v) { t[where] = v; });
-    }
+    put(t, v);
     __syncthreads();
-    for (int k = wave; k < tiles; k += kWaves) {
-      const Place at = place_of(k, blocks);
-      each_place(at, tile_product(t, p, at, side), [&](int, int, int where, double v) { g[where] = v; });
-    }
+    v = tile_product<B>(t, p, ti, tj);
+    put(g, v);
     __syncthreads();
   }
   double* out = reinterpret_cast<double*>(ws + l.rest);
   for (int e = threadIdx.x; e < kSide * kSide; e += kThreads) {
     const int i = e / kSide, j = e % kSide;
-    out[e] = i < side && j < side ? q[i * kPitch + j] * (f * (double)a.scale) : 0.0;
+    out[e] = i < kWidth && j < kWidth ? q[i * kPitch + j] * (f * (double)a.scale) : 0.0;
   }
 }
 
@@ -275,7 +259,15 @@ hipError_t launch_ortho_narrow(int dtype, const OrthoArgs& a, const OrthoLayout&
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     narrow_gram_kernel<T><<<dim3((unsigned)l.splits, count), 256, 0, st>>>(a, l);
-    narrow_steps_kernel<<<(unsigned)count, kThreads, 0, st>>>(a, l);
+    const int64_t blocks = ceil_div(std::min(a.rows, a.cols), 16);
+    if (blocks == 1)
+      narrow_steps_kernel<1><<<(unsigned)count, 64 * tiles_of<1>, 0, st>>>(a, l);
+    else if (blocks == 2)
+      narrow_steps_kernel<2><<<(unsigned)count, 64 * tiles_of<2>, 0, st>>>(a, l);
+    else if (blocks == 3)
+      narrow_steps_kernel<3><<<(unsigned)count, 64 * tiles_of<3>, 0, st>>>(a, l);
+    else
+      narrow_steps_kernel<4><<<(unsigned)count, 64 * tiles_of<4>, 0, st>>>(a, l);
     narrow_apply_kernel<T><<<dim3(chunks, count), 256, 0, st>>>(a, l);
     return hipGetLastError();
   });

@@ -13,8 +13,8 @@
 // moving on by one each row, so the sums stay in registers (loads need no
 // alignment on gfx950, and the lanes of a wave read neighbouring vectors).
 // Buckets are runs of diagonals, summed by a second kernel.  Both are bound by
-// HBM: 32 x 16 x 512 x 512 bf16, forward 98 us (537 MB, 5.5 TB/s), gradient 61 + 6
-// us (268 MB, 4.4 TB/s).  16 lanes a row instead of 64 in the gradient: 103 us
+// HBM: 32 x 16 x 512 x 512 bf16, forward 99 us (537 MB, 5.4 TB/s), gradient 63 + 7
+// us (268 MB, 4.3 TB/s).  16 lanes a row instead of 64 in the gradient: 103 us
 // against 71 in all; rows of a tile in units of 64: 3 x 12 x 127 x 131 fp32 12 us
 // against 7 with 16 (an eighth of the workgroups).
 #include <hip/hip_runtime.h>

@@ -11,8 +11,8 @@
 // like the layer norm: `LPR` lanes hold a row in registers, NV pieces of a
 // vector of x each, so every operand is read once, and the next row's loads are
 // on their way while one is worked on.  bf16, 65536 x 1024: forward with the rows
-// in 8 bits too 113 us (606 MB, 5.4 TB/s), backward with dh 98 + 4 us (537 MB, 5.5
-// TB/s); fp16 beside an fp32 stream, 8191 x 4096: 78 us (403 MB, 5.2 TB/s).  One
+// in 8 bits too 120 us (606 MB, 5.1 TB/s), backward with dh 102 + 5 us (537 MB, 5.3
+// TB/s); fp16 beside an fp32 stream, 8191 x 4096: 83 us (403 MB, 4.9 TB/s).  One
 // row: 4.4 us, its call 12.
 #include <hip/hip_runtime.h>
 

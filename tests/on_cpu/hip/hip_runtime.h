@@ -254,6 +254,12 @@ __forceinline__ int __shfl_up(int v, unsigned by) {
 __forceinline__ float __shfl_xor(float v, unsigned by) {
   return __builtin_bit_cast(float, on_cpu::exchange(__builtin_bit_cast(uint32_t, v), on_cpu::lane_id() ^ by));
 }
+__forceinline__ double __shfl_xor(double v, unsigned by) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, v);
+  const unsigned from = on_cpu::lane_id() ^ by;
+  const uint64_t low = on_cpu::exchange((uint32_t)w, from), high = on_cpu::exchange((uint32_t)(w >> 32), from);
+  return __builtin_bit_cast(double, high << 32 | low);
+}
 inline int __popcll(uint64_t x) { return __builtin_popcountll(x); }
 inline int32_t atomicAdd(int32_t* p, int32_t v) {
   const int32_t old = *p;

@@ -45,6 +45,8 @@ def test_relative_bias(program, batch, heads, queries, keys, offset, buckets, re
     (2, 5, 9, BF16, BF16, 5),
     (1, 30, 130, F16, F16, 5),
     (2, 200, 64, F32, F16, 4),
+    (1, 48, 50, BF16, F32, 5),
+    (1, 17, 300, F32, F32, 1),
     (1, 65, 66, F32, F32, 5),
     (1, 140, 20, F32, F32, 2),
     (1, 140, 131, F32, BF16, 1),
