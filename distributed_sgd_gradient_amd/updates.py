@@ -41,6 +41,29 @@ def _coefficients(coefficients, steps):
     return (ctypes.c_double * (3 * steps))(*[float(v) for c in k for v in c])
 
 
+def _apart(calls, x_size, out_size, workspace):
+    """Refuses what only the calls of different shapes together overwrite: a
+    matrix that another call writes before it is read, or an output twice.  (A
+    call of its own looks at its own matrices.)"""
+    spans = []
+    for (rows, cols, stride, out_stride), (x, y) in calls.items():
+        x_bytes = ((rows - 1) * stride + cols) * x_size
+        out_bytes = ((rows - 1) * out_stride + cols) * out_size
+        for a, b in zip(x, y):
+            if a != b or stride != out_stride or x_size != out_size:  # not in place
+                spans.append((a, a + x_bytes, False, "update"))
+            spans.append((b, b + out_bytes, True, "out"))
+    if workspace is not None and _size(workspace):
+        spans.append((workspace.data_ptr(), workspace.data_ptr() + _size(workspace), True, "workspace"))
+    ends = [0, 0]  # of what is read, of what is written, up to here
+    names = ["", ""]
+    for begin, end, written, name in sorted(spans):
+        if begin < ends[1] or written and begin < ends[0]:
+            raise ValueError(f"{name} overlaps {names[1 if begin < ends[1] else 0]} of another matrix")
+        if end > ends[written]:
+            ends[written], names[written] = end, name
+
+
 def orthogonalize(update, *, steps=STEPS, coefficients=COEFFICIENTS, eps=1e-7, scale=1.0, dtype=None, out=None,
                   workspace=None, stream=None):
     """Matrices brought near the closest orthogonal ones by Newton-Schulz steps,
@@ -101,6 +124,8 @@ def orthogonalize(update, *, steps=STEPS, coefficients=COEFFICIENTS, eps=1e-7, s
             x, y = calls.setdefault((rows, cols, stride, out_stride), ([], []))
             x += at
             y += to
+        if len(calls) > 1 and (outs is not None or workspace is not None):
+            _apart(calls, given[0].element_size(), results[0].element_size(), workspace)
         needs = [_native.check(L.adasum_orthogonalize_workspace_bytes(len(x), rows, cols, out_code))
                  for (rows, cols, _, _), (x, _) in calls.items()]
         ws = _workspace(workspace, max(needs), dev)

@@ -732,3 +732,19 @@ def test_timed(gpu):
     run()
     times = _native.profile_end()
     assert {k: v["launches"] for k, v in times.items()} == {"norm": 2, "bias": 2, "orthogonal": 1}
+
+
+def test_lists_whose_calls_would_overwrite_each_other_are_refused(gpu):
+    flush_print("outputs over another shape's matrices")
+    raw = torch.randn(4096, device="cuda")
+    a, b = raw[:60].view(6, 10), raw[64:164].view(10, 10)
+    free = raw[1024:1124].view(10, 10)
+    before = raw.clone()
+    with pytest.raises(ValueError, match="overlaps"):
+        A.orthogonalize([a, b], out=[raw[100:160].view(6, 10), free])
+    with pytest.raises(ValueError, match="overlaps"):
+        A.orthogonalize([a, b], out=[raw[2000:2060].view(6, 10), raw[2050:2150].view(10, 10)])
+    assert torch.equal(raw, before)
+    want = A.orthogonalize([a, b])
+    got = A.orthogonalize([a, b], out=[a, b])
+    assert got[0] is a and torch.equal(a, want[0]) and torch.equal(b, want[1])

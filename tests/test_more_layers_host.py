@@ -237,3 +237,19 @@ def test_python_refuses():
                  lambda: A.relative_bias_grad(s, 32), lambda: A.orthogonalize(x), lambda: A.orthogonalize([x, x])):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_matrices_of_other_shapes_stay_apart():
+    from distributed_sgd_gradient_amd.updates import _apart
+
+    small, large = (4, 8, 8, 8), (8, 8, 8, 8)  # 128 and 256 bytes of fp32
+    _apart({small: ([0], [0]), large: ([128], [128])}, 4, 4, None)  # in place, one behind the other
+    _apart({small: ([0], [1024]), large: ([0], [2048])}, 4, 4, None)  # one input read twice
+    for x, y in (([0, 128], [128, 1024]), ([0, 128], [1024, 124]), ([0, 512], [1024, 1148])):
+        with pytest.raises(ValueError, match="overlaps"):
+            _apart({small: (x[:1], y[:1]), large: (x[1:], y[1:])}, 4, 4, None)
+    space = torch.empty(64, dtype=torch.uint8)
+    at = space.data_ptr()
+    _apart({small: ([at - 128], [at - 128]), large: ([at + 64], [at + 64])}, 4, 4, space)
+    with pytest.raises(ValueError, match="overlaps"):
+        _apart({small: ([at - 128], [at - 128]), large: ([at + 60], [at + 60])}, 4, 4, space)
