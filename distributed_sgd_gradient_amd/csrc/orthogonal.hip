@@ -251,16 +251,17 @@ __device__ __forceinline__ int across_key(int row) {
 // a step ahead of the products.  Rows of 128 bytes, not of 64 (24 x 1024 x 1024
 // bf16: A 39 us against 45, X 110 against 121); tiles of X written from the
 // registers, 64 bytes a row, not through LDS: X 100 us against 96.
-template <int KIND, int PARTS, int T>
+template <int KIND, int PARTS, int T, int DEEP>
 __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(OrthoArgs a, OrthoLayout l, OrthoStep step) {
   using S = Tile<T, PARTS>;
   constexpr bool APPLY = KIND == kApplyB || KIND == kLastB;
   constexpr int kWaves = S::kWavesP * S::kWavesQ;
   constexpr int WP = T / S::kWavesP, WQ = T / S::kWavesQ, MP = WP / 16, MQ = WQ / 16;
   constexpr int kPieces = T * kStep / 8;  // 16-byte pieces of an operand's part
+  constexpr int kStages = S::kStages * DEEP;
   constexpr int kFills = kPieces / 64 / kWaves, kLoads = 2 * PARTS * kFills;
   static_assert(kFills * kWaves * 64 == kPieces, "whole waves");
-  __shared__ v4u lds[S::kStages][2 * PARTS][kPieces];  // of each step P's parts, then Q's
+  __shared__ v4u lds[kStages][2 * PARTS][kPieces];  // of each step P's parts, then Q's
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // Workgroups are dealt to the eight XCDs in turn: each takes a run of
@@ -439,7 +440,6 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
           acc[i][2 * j + e / 4][e % 4] = __builtin_fmaf(factor[i] * kScaleB, (float)x[e], acc[i][2 * j + e / 4][e % 4]);
       }
   };
-  constexpr int kStages = S::kStages;
   const std::integral_constant<int, 0> first_half;
   const std::integral_constant<int, 1> second_half;
 #pragma unroll
@@ -644,7 +644,15 @@ hipError_t product(const OrthoArgs& a, const OrthoLayout& l, OrthoStep step, int
   step.tiles = KIND == kGramX || KIND == kSquareA ? side * (side + 1) / 2 : side * (uint32_t)(l.m / T);
   step.blocks = step.tiles * step.parts;
   constexpr int kThreads = threads_of<T, PARTS>;
-  product_kernel<KIND, PARTS, T><<<step.blocks * count, kThreads, 0, st>>>(a, l, step);
+  // Two parts an operand leave LDS for two steps where two workgroups share a CU;
+  // of one a CU, four hide the loads' way (1 x 1024 x 1024 fp32: 231 us against
+  // 246.  One part has four already; with eight 160 against 152)
+  if constexpr (T == 64 && PARTS == 2)
+    if (step.blocks * count <= kCUs) {
+      product_kernel<KIND, PARTS, T, 2><<<step.blocks * count, kThreads, 0, st>>>(a, l, step);
+      return hipGetLastError();
+    }
+  product_kernel<KIND, PARTS, T, 1><<<step.blocks * count, kThreads, 0, st>>>(a, l, step);
   return hipGetLastError();
 }
 
