@@ -185,19 +185,33 @@ __device__ __forceinline__ float dpp(float x) {
   return __builtin_bit_cast(float, dpp<kCtrl>(__builtin_bit_cast(uint32_t, x)));
 }
 
+template <int kCtrl>
+__device__ __forceinline__ double dpp(double x) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, (uint64_t)dpp<kCtrl>((uint32_t)(w >> 32)) << 32 | dpp<kCtrl>((uint32_t)w));
+}
+
 __device__ __forceinline__ float lane_value(float x, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)w, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(w >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // The sum over 16 neighbouring lanes or over the wave's 64, in a fixed order,
 // the same in every lane.
-__device__ __forceinline__ float sum16(float x) {
+template <typename F>
+__device__ __forceinline__ F sum16(F x) {
   x += dpp<kXor1>(x);
   x += dpp<kXor2>(x);
   x += dpp<kHalfMirror>(x);
   return x + dpp<kMirror>(x);
 }
-__device__ __forceinline__ float wave_sum(float x) {
+template <typename F>
+__device__ __forceinline__ F wave_sum(F x) {
   x = sum16(x);
   return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
 }

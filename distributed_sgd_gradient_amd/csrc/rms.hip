@@ -12,11 +12,17 @@
 // vector of x each, so every operand is read once, and the next row's loads are
 // on their way while one is worked on.  bf16, 65536 x 1024: forward with the rows
 // in 8 bits too 120 us (606 MB, 5.1 TB/s), backward with dh 102 + 5 us (537 MB, 5.3
-// TB/s); fp16 beside an fp32 stream, 8191 x 4096: 83 us (403 MB, 4.9 TB/s).  One
-// row: 4.4 us, its call 12.
+// TB/s); fp16 beside an fp32 stream, 8191 x 4096: 85 us (403 MB, 4.7 TB/s).  One
+// row: 4.7 us, its call 13.
+//
+// The forward pass has time for more than fp32 beside its loads: squares are
+// summed in fp64 and y carries what its first product leaves out, so rstd and y
+// are rounded once, and the codes are those of the exact rows (in fp32 alone: 120
+// us against 121, 83 against 85; one of some 10^5 codes differs).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "elem.h"
 #include "layer_ops.h"
@@ -52,15 +58,23 @@ __device__ __forceinline__ float rounded(float v) {
   return v;
 }
 
+// v (r + rest) w, rounded once: what the first product leaves out is added to
+// the second, where an infinite w times it must not be of the other sign.
+__device__ __forceinline__ float scaled(float v, float r, float rest, float w) {
+  const float n = v * r, out = __builtin_fmaf(v, rest, __builtin_fmaf(v, r, -n));
+  return __builtin_fmaf(n, w, __builtin_amdgcn_fmed3f(out * w, -FLT_MAX, FLT_MAX));
+}
+
 template <typename T, typename R, int LPR, int NV, bool PACK>
 __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void rms_kernel(RmsArgs a) {
   constexpr int VEC = Type<T>::kVec;
   constexpr int ROWS = LPR < 256 ? 256 / LPR : 1;
-  __shared__ float lds[2][1][LPR / 64 > 0 ? LPR / 64 : 1];
+  __shared__ double lds[2][1][LPR / 64 > 0 ? LPR / 64 : 1];
   const int lane = threadIdx.x & (LPR - 1);
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
   const int H = a.hidden;
+  const double inv_h = 1.0 / (double)H;
   int valid[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) valid[j] = H - (j * LPR + lane) * VEC;
@@ -102,20 +116,29 @@ __global__ __launch_bounds__(LPR < 256 ? 256 : LPR) void rms_kernel(RmsArgs a) {
       }
     }
     if (r + step < a.rows) fetch(r + step);  // in flight behind this row's arithmetic
-    float s[1] = {0.f};
+    double s[1] = {0.0}, odd = 0.0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s[0] = __builtin_fmaf(v[j][i], v[j][i], s[0]);  // zeros outside the row
+      for (int i = 0; i < VEC; i += 2) {  // zeros outside the row
+        s[0] = __builtin_fma((double)v[j][i], (double)v[j][i], s[0]);
+        odd = __builtin_fma((double)v[j][i + 1], (double)v[j][i + 1], odd);
+      }
+    s[0] += odd;
     row_sum<LPR, 1>(s, lds, slot);
     slot ^= 1;
-    const float rstd = inverse_root(s[0] / (float)H + a.eps);
+    // rstd + rest: the estimate's Newton step in fp64 (a sum above fp32's range: 0)
+    const double mean = s[0] * inv_h + (double)a.eps;
+    const float near = inverse_root(s[0] > (double)FLT_MAX ? __builtin_inff() : (float)mean);
+    const double root = __builtin_fma(0.5 * near, __builtin_fma(-mean * near, (double)near, 1.0), (double)near);
+    const bool some = near != 0.f;
+    const float rstd = some ? (float)root : near, rest = some ? (float)(root - (double)rstd) : 0.f;
     if (lane == 0) a.rstd[r] = rstd;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * LPR + lane) * VEC;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[j][i] = i < valid[j] ? rounded(v[j][i] * rstd * w[j][i]) : 0.f;
+      for (int i = 0; i < VEC; ++i) v[j][i] = i < valid[j] ? rounded(scaled(v[j][i], rstd, rest, w[j][i])) : 0.f;
       if (y) store_vec(y + r * a.y_stride + c, v[j], valid[j]);
       if constexpr (PACK) {
         // the codes are those of y as it is stored

@@ -16,8 +16,8 @@ using namespace elem;
 // Sums of N values over the LPR lanes of a row, the same in every lane.
 // `slot` alternates between two LDS areas, so that one barrier a call is
 // enough: an area is written again only after the barrier of the call between.
-template <int LPR, int N>
-__device__ __forceinline__ void row_sum(float (&s)[N], float (*lds)[N][LPR / 64 > 0 ? LPR / 64 : 1], int slot) {
+template <int LPR, int N, typename F>
+__device__ __forceinline__ void row_sum(F (&s)[N], F (*lds)[N][LPR / 64 > 0 ? LPR / 64 : 1], int slot) {
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = LPR == 16 ? sum16(s[i]) : wave_sum(s[i]);
   if constexpr (LPR > 64) {
@@ -29,7 +29,7 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float (*lds)[N][LPR / 64 
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float t = 0.f;
+      F t = 0;
 #pragma unroll
       for (int w = 0; w < LPR / 64; ++w) t += lds[slot][i][w];
       s[i] = t;

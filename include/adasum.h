@@ -221,8 +221,9 @@ ADASUM_API int64_t adasum_sum_workspace_bytes(int K, int64_t N, int dtype);
  *     element.
  *   - dtype, param_dtype, grad_dtype, ... are adasum_dtype_t.  Arithmetic is
  *     fp32, results are rounded once to nearest even; sums over rows are fp32
- *     in pieces of at most 2048 rows (embedding), 16384 (layer norm) or 65536
- *     (linear), joined in fp64.
+ *     in pieces of at most 2048 rows (embedding), 16384 (the norms), 65536
+ *     (linear) or 4096 rows of a diagonal (relative bias), joined in fp64.
+ *     adasum_orthogonalize has arithmetic of its own, given there.
  *   - accumulate != 0 adds the gradient to what dweight, dbias or grad holds
  *     (the microbatches of one step) instead of replacing it.
  *   - Zero rows (or tokens) are allowed: gradients are then zero (unchanged
@@ -369,8 +370,8 @@ ADASUM_API int adasum_linear_grad(const void* dy, int64_t rows, int64_t out_feat
 /*
  * adasum_rms - root-mean-square norm of a residual stream's rows:
  * h = x + residual, rounded to the stream's type, rstd = 1 / sqrt(mean(h^2) +
- * eps), y = h * rstd * weight.  Where a row's squares pass fp32's range, rstd
- * is 0.
+ * eps), y = h * rstd * weight.  Squares are summed in fp64, rstd and y rounded
+ * once.  Where a row's sum of squares passes fp32's range, rstd is 0.
  *
  *   x, y         rows x hidden elements of dtype, hidden <= 16384.
  *   residual, h  rows x hidden elements of stream_dtype: dtype or fp32.  h may

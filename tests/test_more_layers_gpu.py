@@ -180,6 +180,29 @@ def test_rms_of_special_rows(gpu):
         assert dx.shape == (0, 90) and not bool(dw.any())
 
 
+@pytest.mark.parametrize("hidden", (7, 256, 1000, 4096, 16383))
+def test_rms_rounds_once(gpu, hidden):
+    """rstd and an fp32 y are off by half a step, 2^-24 of the value, and what
+    terms of 2^-24 of 2^-24 leave: below 2^-44."""
+    x, w = randn(350, 37, hidden, dtype=F32) * 3, randn(351, hidden, dtype=F32)
+    y, _, rstd = A.rms_norm(x, w)
+    eps = float(torch.tensor(1e-6))
+    r = (x.double().square().mean(1) + eps).rsqrt()
+    bound = 2.0 ** -24 + 2.0 ** -44
+    within(rstd, r, bound * r, "rstd")
+    want = x.double() * r[:, None] * w.double()
+    within(y, want, bound * want.abs(), "y")
+
+
+def test_rms_of_infinite_weights(gpu):
+    x = randn(352, 4, 100, dtype=F32)
+    w = torch.ones(100, device="cuda")
+    w[3], w[4] = float("inf"), float("-inf")
+    y = A.rms_norm(x, w)[0]
+    assert torch.equal(y[:, 3], x[:, 3].sign() * w[3]) and torch.equal(y[:, 4], x[:, 4].sign() * w[4])
+    assert bool(y[:, 5:].isfinite().all())
+
+
 def test_rms_grad_sums_are_bounded(gpu):
     """As for the layer norm: a sum takes 1024 terms, 2 steps across the wave
     and 3 other waves at most, whatever the number of rows."""
