@@ -128,6 +128,7 @@ constexpr int64_t kMaxReach = int64_t(1) << 30;
 struct BiasBuckets {
   int both;  // the keys behind the query have buckets of their own, side ..
   int side;  // buckets of a side
+  uint32_t far;  // the last one's border
   uint32_t border[kMaxBuckets];
 };
 BiasBuckets bias_buckets(int buckets, int64_t reach, bool both);
@@ -159,11 +160,12 @@ struct BiasGradArgs {
   int accumulate;
   float* partials;
 };
-// Workgroups of the gradient: tiles of diagonals, heads, and splits of the rows.
+// Workgroups of the gradient: tiles of diagonals, heads, and splits of the rows;
+// and of the join, where a bucket is cut into pieces of `piece` diagonals.
 struct BiasGradLayout {
   int lanes;  // that share a row
-  int64_t tiles, splits, blocks;
-  size_t bytes;
+  int64_t tiles, splits, blocks, piece, piece_blocks;
+  size_t sums, bytes;  // the pieces' sums begin at `sums`
 };
 BiasGradLayout bias_grad_layout(int64_t batch, int64_t heads, int64_t queries, int64_t keys, int dtype);
 hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st);

@@ -612,8 +612,8 @@ int check_bias_grad(int64_t batch, int64_t heads, int64_t queries, int64_t keys,
                     size_t* bytes) {
   const int64_t rows = batch * heads * queries;
   RETURN_IF(check_matrix(rows, keys, stride, dtype, "dscores", bytes));
-  if (bias_grad_layout(rows == 0 ? 0 : batch, heads, std::max<int64_t>(queries, 1), keys, dtype).blocks >= kMaxBlocks ||
-      heads * kMaxBuckets >= kMaxBlocks)
+  const BiasGradLayout l = bias_grad_layout(rows == 0 ? 0 : batch, heads, std::max<int64_t>(queries, 1), keys, dtype);
+  if (l.blocks >= kMaxBlocks || l.piece_blocks >= kMaxBlocks || heads * kMaxBuckets >= kMaxBlocks)
     return fail(ADASUM_EINVAL, "relative bias: the scores are too large for one call");
   return ADASUM_OK;
 }

@@ -35,6 +35,11 @@ using namespace elem;
 constexpr int kTileRows = 16, kTileCols = 1024;  // of the forward pass
 constexpr int kPieces = 4;                       // pieces a lane has in flight
 constexpr int kGradUnit = 16, kGradAhead = 8;   // rows of a unit, rows in flight
+// A bucket of more sums of diagonals than this is joined in pieces, by two
+// launches: 64 x 16 x 1 x 4096 bf16 takes 18 us a call (one workgroup a bucket 42),
+// 1 x 16 x 1 x 2^20 122 (6263).  Below it the second launch costs more
+// than it saves: 32 x 16 x 512 x 512, 12288 sums, 70 us against 74.
+constexpr int64_t kJoinValues = 16384, kPieceValues = 4096;
 
 // The bucket of distance n on its side: the last border at or below n.
 __device__ __forceinline__ int bucket_of(const BiasBuckets& k, uint32_t n) {
@@ -73,9 +78,15 @@ __global__ __launch_bounds__(256) void bias_kernel(BiasArgs a, BiasLayout l) {
   const int64_t i0 = row_tile * kTileRows, j0 = col_tile * kTileCols;
   const int rows = (int)min<int64_t>(kTileRows, a.queries - i0), cols = (int)min<int64_t>(kTileCols, a.keys - j0);
   // line[k] is the bias at key - query = first + k
-  const int64_t first = j0 - (i0 + rows - 1) - a.offset;
-  for (int k = threadIdx.x; k < rows + cols - 1; k += 256)
-    line[line_at(k)] = load_any(a.table, a.table_dtype, (int64_t)bucket_at(a.buckets, first + k) * a.table_stride + head);
+  const int64_t first = j0 - (i0 + rows - 1) - a.offset, last = first + rows + cols - 2;
+  // all of them in a side's last bucket, as most are of long rows: no search
+  const int64_t far = a.buckets.far;
+  const bool before = last <= -far, behind = a.buckets.both && first >= far;
+  const int all = before ? a.buckets.side - 1 : behind ? 2 * a.buckets.side - 1 : -1;
+  for (int k = threadIdx.x; k < rows + cols - 1; k += 256) {
+    const int b = all >= 0 ? all : bucket_at(a.buckets, first + k);
+    line[line_at(k)] = load_any(a.table, a.table_dtype, (int64_t)b * a.table_stride + head);
+  }
   __syncthreads();
   const int64_t n_begin = part * l.part_batch, n_end = min(a.batch, n_begin + l.part_batch);
   const uint32_t per_row = (uint32_t)(cols + VEC - 1) / VEC, per_batch = per_row * rows;
@@ -197,51 +208,115 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(BiasGradArgs a, BiasGrad
   }
 }
 
-// dtable[b][h]: bucket b's diagonals of every split, summed in fp64 by a
-// workgroup in a fixed order: 64 diagonals and four splits at a time.
-__global__ __launch_bounds__(256) void bias_join_kernel(BiasGradArgs a, int splits) {
-  __shared__ double sums[256];
-  const int64_t head = blockIdx.x % (uint32_t)a.heads;
-  const int b = blockIdx.x / (uint32_t)a.heads;
+// The diagonals of bucket b, first to last (none: first > last).
+__host__ __device__ inline void diagonals_of(const BiasGradArgs& a, int b, int64_t* first, int64_t* last) {
   const BiasBuckets& k = a.buckets;
   const bool ahead = k.both && b >= k.side;  // keys behind the query
   const int s = ahead ? b - k.side : b;
-  const int64_t near = k.border[s], far = s + 1 < k.side ? k.border[s + 1] : int64_t(1) << 40;  // near <= n < far
+  const int64_t beyond = int64_t(1) << 40;
+  const int64_t near = k.border[s], far = s + 1 < k.side ? (int64_t)k.border[s + 1] : beyond;  // near <= n < far
   // as key - query, both ends included
   int64_t lo, hi;
   if (ahead) {
-    lo = max<int64_t>(near, 1);
+    lo = near > 1 ? near : 1;
     hi = far - 1;
   } else {
     lo = -(far - 1);
-    hi = !k.both && s == 0 ? int64_t(1) << 40 : -near;
+    hi = !k.both && s == 0 ? beyond : -near;
   }
-  const int64_t diagonals = a.queries + a.keys - 1, zero = a.queries - 1 + a.offset;
-  lo = max<int64_t>(lo + zero, 0);
-  hi = min(hi + zero, diagonals - 1);
-  const int64_t pitch = a.heads * diagonals;
+  const int64_t zero = a.queries - 1 + a.offset, end = a.queries + a.keys - 2;
+  *first = lo + zero > 0 ? lo + zero : 0;
+  *last = hi + zero < end ? hi + zero : end;
+}
+
+// A lane's share of a head's diagonals lo to hi of every split: the workgroup
+// takes 256 / G diagonals of G splits at a time, a lane eight of these at once,
+// of V splits G apart.  What lies past the last is read at the last.
+template <int G, int V>
+__device__ __forceinline__ double lane_sum(const float* from, int64_t pitch, int splits, int64_t lo, int64_t hi) {
+  constexpr int U = 8 / V, WIDTH = 256 / G;
   double t = 0.0;
-  for (int64_t d = lo + (threadIdx.x & 63); d <= hi; d += 64) {
-    const float* p = a.partials + head * diagonals + d;
-    for (int first = threadIdx.x >> 6; first < splits; first += 32) {
-      float v[8];  // splits past the last are read at the last: eight loads at once
+  for (int64_t d = lo + threadIdx.x % WIDTH; d <= hi; d += U * WIDTH)
+    for (int first = threadIdx.x / WIDTH; first < splits; first += G * V) {
+      float v[U][V];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = p[min(first + 4 * u, splits - 1) * pitch];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int u = 0; u < 8; ++u) t += first + 4 * u < splits ? (double)v[u] : 0.0;
+        for (int w = 0; w < V; ++w) v[u][w] = from[min(first + G * w, splits - 1) * pitch + min(d + WIDTH * u, hi)];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int w = 0; w < V; ++w)
+          t += d + WIDTH * u <= hi && first + G * w < splits ? (double)v[u][w] : 0.0;
     }
-  }
-  sums[threadIdx.x] = t;
+  return t;
+}
+
+// The sum in fp64 by a workgroup in a fixed order; the result in lane 0.
+__device__ __forceinline__ double sum_diagonals(const BiasGradArgs& a, int splits, int64_t head, int64_t lo,
+                                                int64_t hi) {
+  __shared__ double sums[256];
+  const int64_t diagonals = a.queries + a.keys - 1, pitch = a.heads * diagonals;
+  const float* from = a.partials + head * diagonals;
+  sums[threadIdx.x] = splits < 4    ? lane_sum<1, 1>(from, pitch, splits, lo, hi)
+                      : splits <= 8   ? lane_sum<4, 2>(from, pitch, splits, lo, hi)
+                      : splits <= 16  ? lane_sum<4, 4>(from, pitch, splits, lo, hi)
+                                      : lane_sum<4, 8>(from, pitch, splits, lo, hi);
   __syncthreads();
   for (int w = 128; w > 0; w /= 2) {
     if ((int)threadIdx.x < w) sums[threadIdx.x] += sums[threadIdx.x + w];
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    const int64_t i = (int64_t)b * a.heads + head;
-    const double sum = sums[0];
-    store_any(a.dtable, a.grad_dtype, i, a.accumulate ? sum + (double)load_any(a.dtable, a.grad_dtype, i) : sum);
-  }
+  return sums[0];
+}
+
+__device__ __forceinline__ void store_bucket(const BiasGradArgs& a, int64_t b, int64_t head, double sum) {
+  const int64_t i = b * a.heads + head;
+  store_any(a.dtable, a.grad_dtype, i, a.accumulate ? sum + (double)load_any(a.dtable, a.grad_dtype, i) : sum);
+}
+
+// dtable[b][h], a workgroup each.
+__global__ __launch_bounds__(256) void bias_join_kernel(BiasGradArgs a, int splits) {
+  const int64_t head = blockIdx.x % (uint32_t)a.heads;
+  const int b = blockIdx.x / (uint32_t)a.heads;
+  int64_t lo, hi;
+  diagonals_of(a, b, &lo, &hi);
+  const double sum = sum_diagonals(a, splits, head, lo, hi);
+  if (threadIdx.x == 0) store_bucket(a, b, head, sum);
+}
+
+// The first piece of every bucket, and behind the last bucket how many there are.
+struct Pieces {
+  uint32_t first[kMaxBuckets + 1];
+};
+
+// A piece's sum, a workgroup each.
+__global__ __launch_bounds__(256) void bias_piece_kernel(BiasGradArgs a, Pieces k, int splits, int64_t length,
+                                                         double* out) {
+  __shared__ int which;
+  const int64_t head = blockIdx.x % (uint32_t)a.heads;
+  const uint32_t piece = blockIdx.x / (uint32_t)a.heads;
+  const int t = threadIdx.x;
+  if (t < a.buckets_total && k.first[t] <= piece && piece < k.first[t + 1]) which = t;
+  __syncthreads();
+  const int b = which;
+  int64_t lo, hi;
+  diagonals_of(a, b, &lo, &hi);
+  lo += (piece - k.first[b]) * length;
+  const double sum = sum_diagonals(a, splits, head, lo, min(hi, lo + length - 1));
+  if (t == 0) out[(int64_t)piece * a.heads + head] = sum;
+}
+
+// dtable[b][h] from its pieces' sums, a wave each.
+__global__ __launch_bounds__(256) void bias_pieces_kernel(BiasGradArgs a, Pieces k, const double* sums) {
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i >= a.buckets_total * a.heads) return;
+  const int64_t b = i / a.heads, head = i - b * a.heads;
+  const uint32_t end = k.first[b + 1];
+  double t = 0.0;
+  for (uint32_t p = k.first[b] + (threadIdx.x & 63); p < end; p += 64) t += sums[(int64_t)p * a.heads + head];
+  t = wave_sum(t);
+  if ((threadIdx.x & 63) == 0) store_bucket(a, b, head, t);
 }
 
 // Whole numbers of any size, for borders that are powers.
@@ -290,6 +365,7 @@ BiasBuckets bias_buckets(int buckets, int64_t reach, bool both) {
     }
     t.border[k] = n;
   }
+  t.far = t.border[m - 1];
   return t;
 }
 
@@ -330,6 +406,12 @@ BiasGradLayout bias_grad_layout(int64_t batch, int64_t heads, int64_t queries, i
   l.splits = std::max<int64_t>({1, std::min(fill, most), ceil_div(units, groups * (4096 / kGradUnit))});
   l.blocks = l.splits * heads * l.tiles;
   l.bytes = (size_t)l.splits * heads * diagonals * sizeof(float);
+  if (l.splits * diagonals > kJoinValues) {
+    l.piece = std::max<int64_t>(64, kPieceValues / l.splits);
+    l.piece_blocks = (kMaxBuckets + diagonals / l.piece) * heads;
+    l.sums = (l.bytes + 7) / 8 * 8;
+    l.bytes = l.sums + (size_t)l.piece_blocks * sizeof(double);
+  }
   return l;
 }
 
@@ -344,7 +426,22 @@ hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st) {
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
-  bias_join_kernel<<<(unsigned)(a.buckets_total * a.heads), 256, 0, st>>>(a, (int)l.splits);
+  Pieces k{};
+  int64_t longest = 0;
+  for (int b = 0; b < a.buckets_total; ++b) {
+    int64_t lo, hi;
+    diagonals_of(a, b, &lo, &hi);
+    const int64_t length = std::max<int64_t>(hi - lo + 1, 0);
+    longest = std::max(longest, length);
+    if (l.piece > 0) k.first[b + 1] = k.first[b] + (uint32_t)ceil_div(length, l.piece);
+  }
+  if (longest * l.splits <= kJoinValues) {
+    bias_join_kernel<<<(unsigned)(a.buckets_total * a.heads), 256, 0, st>>>(a, (int)l.splits);
+  } else {
+    double* sums = reinterpret_cast<double*>(reinterpret_cast<char*>(a.partials) + l.sums);
+    bias_piece_kernel<<<(unsigned)(k.first[a.buckets_total] * a.heads), 256, 0, st>>>(a, k, (int)l.splits, l.piece, sums);
+    bias_pieces_kernel<<<(unsigned)ceil_div(a.buckets_total * a.heads, 4), 256, 0, st>>>(a, k, sums);
+  }
   return hipGetLastError();
 }
 

@@ -35,6 +35,9 @@ def test_rms(program, rows, hidden, dtype):  # noqa: F811
     (2, 1, 130, 141, 0, 32, 128, 1),
     (1, 1, 18, 1100, -30, 64, 300, 1),
     (1, 1, 300, 3, 1000000000, 32, 128, 1),
+    # buckets joined in pieces: of few splits, and of eight or more
+    (1, 2, 3, 17001, 40, 32, 128, 1),
+    (1, 1, 600, 2001, -3, 8, 20, 0),
 ])
 def test_relative_bias(program, batch, heads, queries, keys, offset, buckets, reach, both, dtype):  # noqa: F811
     run(program("relative_bias"), batch, heads, queries, keys, offset, buckets, reach, both, dtype)

@@ -340,6 +340,35 @@ def test_relative_bias_far_and_empty(gpu):
     assert torch.equal(A.relative_bias(table, 3, 4, offset=-far), table[31][:, None, None].expand(2, 3, 4))
 
 
+@pytest.mark.parametrize("batch,heads,queries,keys,offset,buckets,reach,both", [
+    (1, 3, 1, 70001, 70000, 32, 128, True),
+    (1, 3, 1, 70001, -300, 32, 128, True),
+    (2, 2, 5, 33000, 20000, 32, 128, True),
+    (1, 1, 700, 2003, 0, 8, 20, False),
+    (3, 1, 1025, 2047, 900, 256, 1000, True),
+    (40, 2, 200, 700, 3, 32, 128, False),
+])
+def test_relative_bias_of_long_rows(gpu, batch, heads, queries, keys, offset, buckets, reach, both):
+    """Tiles in one bucket, and buckets joined in pieces."""
+    flush_print(f"long rows {batch}x{heads}x{queries}x{keys} {offset} {buckets} {reach} {both}")
+    of = bucket_matrix(queries, keys, offset, buckets, reach, both)
+    kind = dict(offset=offset, bidirectional=both, max_distance=reach)
+    table = randn(363, buckets, heads)
+    assert torch.equal(A.relative_bias(table, queries, keys, **kind), table.t()[:, of])
+    ds = randn(364, batch, heads, queries, keys)
+    flat = ds.double().reshape(batch, heads, -1)
+
+    def sums(t):
+        return torch.zeros(heads, buckets, dtype=torch.float64, device="cuda").index_add_(1, of.reshape(-1), t.sum(0)).t()
+    want, mag = sums(flat), sums(flat.abs())
+    got = A.relative_bias_grad(ds, buckets, **kind)
+    within(got, want, (min(batch * queries, 4096) + 17) * E * mag + 2 * E * want.abs(), "dtable")
+    assert torch.equal(A.relative_bias_grad(ds, buckets, **kind), got)
+    seg = torch.full((buckets, heads), 1.5, device="cuda")
+    A.relative_bias_grad(ds, buckets, out=seg, accumulate=True, **kind)
+    within(seg, want + 1.5, (min(batch * queries, 4096) + 17) * E * mag + 2 * E * (want + 1.5).abs(), "added")
+
+
 def test_relative_bias_grad_keeps_nan_in_its_bucket(gpu):
     ds = randn(361, 2, 3, 50, 60)
     want = A.relative_bias_grad(ds, 32)
