@@ -6,7 +6,7 @@
 
 Compiles every source under ``csrc/`` with hipcc for gfx950, up to four at a
 time, and links one shared library next to this file.  Always recompiles (the
-build takes under a minute).
+build takes about a minute).
 """
 
 import os

@@ -172,7 +172,10 @@ hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st);
 
 // ---------------------------------------------------------------- orthogonal updates
 
-constexpr int kOrthoTogether = 32;  // matrices of one launch at most
+// Matrices of one launch at most.  A narrow one takes its steps in a workgroup,
+// so more fill the card (96 of 64 x 1024 fp32: 114 us, 32 at a time 226); of wide
+// ones 32 do, and their workspaces grow.
+constexpr int kOrthoTogether = 128, kOrthoWide = 32;
 constexpr size_t kOrthoWorkspace = size_t(4) << 30;  // and no more than this takes, if it is two or more
 constexpr int kOrthoSteps = 16;
 constexpr int64_t kMaxOrthoSide = int64_t(1) << 15;

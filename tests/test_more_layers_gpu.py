@@ -489,6 +489,14 @@ def test_orthogonalize_one_step_and_own_coefficients(gpu):
     within(eye, torch.eye(90, dtype=torch.float64), 1e-4, "orthogonal")
 
 
+def test_orthogonalize_more_than_a_launch_takes(gpu):
+    flush_print("131 matrices of 16 x 30")
+    x = spectrum(429, 16, 30, F32, count=131)
+    got = A.orthogonalize(x)
+    for i in (0, 127, 128, 130):
+        assert torch.equal(A.orthogonalize(x[i]), got[i])
+
+
 def test_orthogonalize_many_and_lists(gpu):
     """Matrices do not notice each other: more than one launch takes, strided,
     in lists of shapes, in place, as segments of one buffer; bitwise."""
