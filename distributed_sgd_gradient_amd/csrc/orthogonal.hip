@@ -7,7 +7,7 @@
 // which takes every singular value s to a s + b s^3 + c s^5.
 //
 // Bound by the matrix cores, the card's power, and X's traffic: 24 matrices of
-// 1024 x 1024 in bf16 take 840 to 860 us, 600 TFLOP/s with half of the symmetric
+// 1024 x 1024 in bf16 take 820 to 850 us, 620 TFLOP/s with half of the symmetric
 // products (a library product of 8192^3 in fp16 reaches 1127).  A step there is 41
 // us of A, 42 of B and 96 of X; the loops alone, whose matrix instructions run at
 // 1.1 PFLOP/s, take 27, 25 and 70, the rest is the writing of the results, which
@@ -51,7 +51,9 @@ typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr float kScaleX = 16384.f, kScaleA = 8192.f, kScaleB = 2048.f;
-constexpr int kSumParts = 64;  // workgroups that sum a matrix's squares
+// Workgroups that sum a matrix's squares (4096 x 1024 fp32: 6 us, with 64 of them
+// 14; 24 x 1024 x 1024 bf16 17 against 15).
+constexpr int kSumParts = 256;
 // bf16 results of sides above this take one part of each operand.  Narrower
 // ones are bound by the launches, and in the smallest the roundings of few
 // values do not average out (5 x 3: 4.9e-3 of the norm).
@@ -123,7 +125,6 @@ __global__ __launch_bounds__(256) void square_sum_kernel(OrthoArgs a, OrthoLayou
 template <typename T>
 __global__ __launch_bounds__(256) void first_kernel(OrthoArgs a, OrthoLayout l) {
   __shared__ float tile[64][65];
-  __shared__ double sums[kSumParts];
   char* ws = a.ws + blockIdx.y * l.per_matrix;
   const uint32_t tiles_m = (uint32_t)(l.m / 64), ti = blockIdx.x / tiles_m, tk = blockIdx.x - ti * tiles_m;
   const int64_t i0 = (int64_t)ti * 64, k0 = (int64_t)tk * 64;
@@ -146,11 +147,11 @@ __global__ __launch_bounds__(256) void first_kernel(OrthoArgs a, OrthoLayout l) 
       for (int e = 0; e < 4; ++e) raw[u][e] = r < a.rows && from + e < a.cols ? p[e] : (T)0.f;
     }
   }
-  if (threadIdx.x < kSumParts) sums[threadIdx.x] = reinterpret_cast<const double*>(ws + l.sums)[threadIdx.x];
-  __syncthreads();
+  const double* sums = reinterpret_cast<const double*>(ws + l.sums) + (threadIdx.x & 63);
   double s = 0.0;
 #pragma unroll
-  for (int i = 0; i < kSumParts; ++i) s += sums[i];
+  for (int i = 0; i < kSumParts / 64; ++i) s += sums[i * 64];
+  s = wave_sum(s);
   const double f = (double)kScaleX / (sqrt(s) + a.eps);
   float v[4][4];
 #pragma unroll
