@@ -9,9 +9,10 @@
 // Bound by the matrix cores, the card's power, and X's traffic: 24 matrices of
 // 1024 x 1024 in bf16 take 820 to 850 us, 620 TFLOP/s with half of the symmetric
 // products (a library product of 8192^3 in fp16 reaches 1127).  A step there is 41
-// us of A, 42 of B and 96 of X; the loops alone, whose matrix instructions run at
-// 1.1 PFLOP/s, take 27, 25 and 70, the rest is the writing of the results, which
-// begins when all workgroups end.  Matrices with a side of at most 64 are in
+// us of A, 42 of B and 96 of X.  The loops alone take 28, 25 and 70 (1.1, 1.3 and
+// 0.74 PFLOP/s); in A and B the results are written when the loops of all
+// workgroups have ended, in X beside loads, which wait for them (with the loads of
+// the first steps only X takes 69 too).  Matrices with a side of at most 64 are in
 // orthogonal_narrow.hip.
 //
 // Products take fp16 operands and sum in fp32.  X is kept as hi + lo, two fp16
