@@ -439,7 +439,8 @@ hipError_t launch_bias_grad(int dtype, const BiasGradArgs& a, hipStream_t st) {
     bias_join_kernel<<<(unsigned)(a.buckets_total * a.heads), 256, 0, st>>>(a, (int)l.splits);
   } else {
     double* sums = reinterpret_cast<double*>(reinterpret_cast<char*>(a.partials) + l.sums);
-    bias_piece_kernel<<<(unsigned)(k.first[a.buckets_total] * a.heads), 256, 0, st>>>(a, k, (int)l.splits, l.piece, sums);
+    const unsigned blocks = (unsigned)(k.first[a.buckets_total] * a.heads);
+    bias_piece_kernel<<<blocks, 256, 0, st>>>(a, k, (int)l.splits, l.piece, sums);
     bias_pieces_kernel<<<(unsigned)ceil_div(a.buckets_total * a.heads, 4), 256, 0, st>>>(a, k, sums);
   }
   return hipGetLastError();

@@ -2,7 +2,8 @@
 microbatch before its gradient is combined with the others'.
 
 Embedding lookup, layer norm, the norm of a residual stream, relative position
-biases, activations kept in 8 bits, and the gradients of the tables and weights, which may be written straight into (or added to) the
+biases, activations kept in 8 bits, and the gradients of the tables and
+weights, which may be written straight into (or added to) the
 segments of a flat gradient buffer that :func:`combine` reads.  As there, only
 argument marshalling happens here; torch provides device memory and streams.
 
