@@ -1,0 +1,86 @@
+"""Orthogonal updates on the GPU where they are hard: low rank over many steps.
+Against the formula in 64 bits; tolerances are counted in roundings."""
+
+import math
+
+import pytest
+import torch
+
+import distributed_sgd_gradient_amd as A
+from conftest import flush_print
+from test_layers_gpu import BF16, DTYPES, F16, F32, gen, ids
+from test_more_layers_gpu import plain_orthogonal
+
+pytestmark = pytest.mark.gpu
+
+DEFAULT = (3.4445, -4.7750, 2.0315)
+STEEP = (4.5, -5.88, 1.54)
+HALF = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}
+
+
+def whole(seed, *shape):
+    return torch.randint(-7, 8, shape, generator=gen(seed)).double()
+
+
+def low_rank(seed, count, n, m, rank, rounded, dtype=F32):
+    """Of exactly that rank, or rounded to it from a product that does not fit."""
+    x = whole(seed, count, n, rank) @ whole(seed + 1, count, rank, m)
+    return (x * (math.pi if rounded else 1.0)).to(dtype).cuda()
+
+
+def off(got, want):
+    got, want = got.double(), want.double()
+    return float(((got - want).flatten(-2).norm(dim=-1) / want.flatten(-2).norm(dim=-1)).max())
+
+
+@pytest.mark.parametrize("out", DTYPES, ids=ids)
+@pytest.mark.parametrize("n,m,rank,rounded,steps,coefficients", [
+    (32, 300, 4, False, 8, [DEFAULT]),
+    (32, 300, 4, False, 9, [DEFAULT]),
+    (32, 300, 4, False, 12, [DEFAULT]),
+    (300, 32, 4, False, 16, [DEFAULT]),
+    (32, 300, 4, True, 10, [DEFAULT]),
+    (61, 769, 8, False, 14, [DEFAULT]),
+    (64, 64, 8, False, 16, [STEEP]),
+    (16, 2000, 2, False, 16, [DEFAULT]),
+    (48, 5000, 3, True, 9, [DEFAULT, STEEP, (1.5, -0.5, 0.0)]),
+    (1, 5, 1, True, 16, [DEFAULT]),
+])
+def test_narrow_low_rank_over_many_steps(gpu, n, m, rank, rounded, steps, coefficients, out):
+    """Off by the result's rounding, by what fp64 leaves where the update has no
+    direction (2^-53 of sums of 64 terms, here and in the reference, raised by a
+    in every step) and, of a rounded update, by 5e-6 of the directions that the
+    steps of one G bring to 1."""
+    flush_print(f"low rank {n}x{m} rank {rank} {steps} steps to {out}")
+    ks = (coefficients * steps)[:steps]
+    x = low_rank(600, 3, n, m, rank, rounded)
+    got = A.orthogonalize(x, steps=steps, coefficients=ks, dtype=out)
+    limit = HALF[out] + 128 * 2.0 ** -53 * math.prod(abs(k[0]) for k in ks) + (5 * 2.0 ** -20 if rounded else 0)
+    far = off(got, plain_orthogonal(x, ks))
+    flush_print(f"  off by {far:.3g} of the norm, limit {limit:.3g}")
+    assert far <= limit
+    # alone, in place, and as a captured graph: the same bits
+    assert torch.equal(A.orthogonalize(x[1], steps=steps, coefficients=ks, dtype=out), got[1])
+    if out == F32:
+        y, z = x.clone(), torch.empty_like(x)
+        assert torch.equal(A.orthogonalize(y, steps=steps, coefficients=ks, out=y), got)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            A.orthogonalize(x, steps=steps, coefficients=ks, out=z)
+        for _ in range(3):
+            z.zero_()
+            g.replay()
+            assert torch.equal(A.orthogonalize(x, steps=steps, coefficients=ks), got)
+            torch.cuda.synchronize()
+            assert torch.equal(z, got)
+
+
+def test_narrow_special_matrices_over_many_steps(gpu):
+    x = low_rank(610, 5, 20, 90, 3, True)
+    want = A.orthogonalize(x, steps=16)
+    x[1] = 0
+    x[2, 3, 4] = float("nan")
+    x[3, 19, 89] = float("inf")
+    got = A.orthogonalize(x, steps=16)
+    assert torch.equal(got[[0, 4]], want[[0, 4]]) and not bool(got[1].any()) and bool(got[2:4].isnan().all())
