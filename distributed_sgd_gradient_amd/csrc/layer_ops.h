@@ -189,23 +189,47 @@ struct OrthoLayout {
   int parts, together;  // together: matrices of one launch
   int tile_a, tile_b, tile_x;  // of the three products of a step
   int splits, split_steps;    // of the sums of X X^T
-  size_t x[2][2], a[2], b[2], rest, sums, partials;  // x: of even and odd steps
+  size_t x[2][2], a[2], b[2], rest, sums, scales, partials;  // x: of even and odd steps
   size_t per_matrix, total;
 };
 OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtype);
+
+// At most what a step makes of singular values s up to `most`, |a s + b s^3 + c
+// s^5|, and what it adds to a, |b s^2 + c s^4|.
+struct OrthoBound {
+  double value, added;
+};
+__host__ __device__ inline OrthoBound ortho_bound(double a, double b, double c, double most) {
+  const double t = most * most;
+  auto image = [&](double u) { return fabs(sqrt(u) * (a + u * (b + u * c))); };  // of s^2 = u
+  auto added = [&](double u) { return fabs(u * (b + u * c)); };
+  OrthoBound most_of{image(t), added(t)};
+  // where a + 3 b u + 5 c u^2 = 0, and where b + 2 c u = 0
+  const double root = 9 * b * b - 20 * a * c;
+  const double at[4] = {c != 0 && root >= 0 ? (-3 * b + sqrt(root)) / (10 * c) : 0,
+                        c != 0 && root >= 0 ? (-3 * b - sqrt(root)) / (10 * c) : 0, b != 0 ? -a / (3 * b) : 0,
+                        c != 0 ? -b / (2 * c) : 0};
+  for (int i = 0; i < 4; ++i)
+    if (at[i] > 0 && at[i] < t) {
+      most_of.value = image(at[i]) > most_of.value ? image(at[i]) : most_of.value;
+      most_of.added = added(at[i]) > most_of.added ? added(at[i]) : most_of.added;
+    }
+  return most_of;
+}
 
 struct OrthoArgs {
   const void* x[kOrthoTogether];
   void* out[kOrthoTogether];
   int64_t rows, cols, x_stride, out_stride;
   int out_dtype, steps;
+  int plain;  // no step leaves all singular values of an X of norm 1 below 1/2
   double eps;
   float scale;
   double coefficients[3 * kOrthoSteps];
   char* ws;
 };
 struct OrthoStep {
-  float a, b, c;
+  int index;
   int from;  // the X to read; the other one is written
   uint32_t tiles, blocks;  // of a matrix: tiles, and workgroups
   int parts, part_steps;

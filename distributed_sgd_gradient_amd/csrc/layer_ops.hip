@@ -717,31 +717,21 @@ int64_t orthogonalize_bytes(int64_t count, int64_t rows, int64_t cols, int out_d
 }
 
 // Follows the largest singular value through the steps: the kernels hold X and
-// B in fp16 parts, whose range they must not leave.
-int check_coefficients(int steps, const double* k) {
+// B in fp16 parts, whose range they must not leave.  *plain: it stays above 1/2.
+int check_coefficients(int steps, const double* k, int* plain) {
+  *plain = 1;
   if (steps < 1 || steps > kOrthoSteps) return fail(ADASUM_EINVAL, "steps must be in [1, 16]");
   if (k == nullptr) return fail(ADASUM_EINVAL, "coefficients is NULL");
   double most = 1.001;  // with room for rounding
   for (int s = 0; s < steps; ++s, k += 3) {
-    const double a = k[0], b = k[1], c = k[2], t = most * most;
+    const double a = k[0], b = k[1], c = k[2];
     if (!std::isfinite((float)a) || !std::isfinite((float)b) || !std::isfinite((float)c))
       return fail(ADASUM_EINVAL, "coefficients must be finite in fp32");
-    auto image = [&](double u) { return std::fabs(std::sqrt(u) * (a + u * (b + u * c))); };  // of s^2 = u
-    auto added = [&](double u) { return std::fabs(u * (b + u * c)); };
-    double x = image(t), y = added(t);
-    // where a + 3 b u + 5 c u^2 = 0, and where b + 2 c u = 0
-    const double root = 9 * b * b - 20 * a * c;
-    double at[4] = {c != 0 && root >= 0 ? (-3 * b + std::sqrt(root)) / (10 * c) : 0,
-                    c != 0 && root >= 0 ? (-3 * b - std::sqrt(root)) / (10 * c) : 0, b != 0 ? -a / (3 * b) : 0,
-                    c != 0 ? -b / (2 * c) : 0};
-    for (double u : at)
-      if (u > 0 && u < t) {
-        x = std::max(x, image(u));
-        y = std::max(y, added(u));
-      }
-    if (!(x <= 1.9) || !(y <= 30.0))
+    const OrthoBound bound = ortho_bound(a, b, c, most);
+    if (!(bound.value <= 1.9) || !(bound.added <= 30.0))
       return fail(ADASUM_EINVAL, "coefficients must keep singular values below 2, and b A + c A^2 below 31");
-    most = std::max(x * 1.01, 1e-3);
+    if (bound.value <= 0.5) *plain = 0;
+    most = std::max(bound.value * 1.01, 1e-3);
   }
   return ADASUM_OK;
 }
@@ -753,7 +743,8 @@ int orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t col
   RETURN_IF(check_ortho(count, rows, cols, out_dtype));
   RETURN_IF(check_matrix(rows, cols, x_stride, dtype, "x", &x_bytes));
   RETURN_IF(check_matrix(rows, cols, out_stride, out_dtype, "out", &out_bytes));
-  RETURN_IF(check_coefficients(steps, coefficients));
+  int plain = 0;
+  RETURN_IF(check_coefficients(steps, coefficients, &plain));
   if (!std::isfinite((float)eps) || (float)eps < FLT_MIN)
     return fail(ADASUM_EINVAL, "eps must be a positive normal fp32 number");
   if (!std::isfinite((float)scale)) return fail(ADASUM_EINVAL, "scale must be finite in fp32");
@@ -780,6 +771,7 @@ int orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t col
   a.out_stride = out_stride;
   a.out_dtype = out_dtype;
   a.steps = steps;
+  a.plain = plain;
   a.eps = eps;
   a.scale = (float)scale;
   for (int i = 0; i < 3 * steps; ++i) a.coefficients[i] = coefficients[i];

@@ -29,7 +29,9 @@
 //
 // Values are scaled by powers of two so that neither part leaves fp16's normal
 // range: the host admits coefficients only that keep singular values below 2
-// and B below 31.
+// and B below 31, and a matrix that is far smaller than eps, or that the steps
+// shrink, has powers of its own (65 x 66 fp32, eps 10^8 of its norm: off by 1e-7
+// of the result's norm, without them by 2e-2).
 //
 // Everything is padded with zeros to whole tiles in the workspace, so the
 // products have no edges.  A and B are symmetric: half of their tiles are
@@ -81,6 +83,46 @@ template <int T, int PARTS>
 constexpr int threads_of = 64 * Tile<T, PARTS>::kWavesP * Tile<T, PARTS>::kWavesQ;
 constexpr int kStep = 64;  // of the sum: rows of 128 bytes, a line of the L2
 constexpr int kXCDs = 8;
+
+// X is held as 2^e X, where its singular values are below 1/2 at most (an update
+// far smaller than eps, coefficients that shrink it): of a step's e to the next
+// one's, and B as 2^f B.  All powers are 1 else.
+struct Scale {
+  float b, c;  // of A as it is held, and of its square
+  float own;   // a 2^f
+  int out;     // the exponent that the sum of both is raised by
+};
+typedef __attribute__((address_space(4))) const Scale* constant_scales;  // read into scalar registers
+
+// v has arrived here, not where it is used first.
+__device__ __forceinline__ void arrived(float& v) {
+  int bits = __builtin_bit_cast(int, v);
+  asm volatile("" : "+r"(bits));
+  v = __builtin_bit_cast(float, bits);
+}
+
+// The least e from 0 on that leaves 2^e s in [1/2, 1).
+__device__ __forceinline__ int room_above(double s) {
+  int k = 0;
+  if (s > 0 && s < 0.5) frexp(s, &k);
+  return -k;
+}
+
+// The powers of all steps for an X whose singular values are at most `most`.
+__device__ void write_scales(const OrthoArgs& a, double most, Scale* to) {
+  int e = room_above(most);
+  for (int s = 0; s < a.steps; ++s) {
+    const double ca = a.coefficients[3 * s], cb = a.coefficients[3 * s + 1], cc = a.coefficients[3 * s + 2];
+    const OrthoBound bound = ortho_bound(ca, cb, cc, most);
+    most = bound.value * 1.01;
+    const int next = s + 1 < a.steps ? room_above(most) : 0;
+    // B is raised no further than it counts beside a, nor above its range
+    int f = room_above(bound.added / 30);
+    if (ca != 0) f = min(f, room_above(fabs(ca)));
+    to[s] = Scale{(float)ldexp(cb, f - 2 * e), (float)ldexp(cc, f - 4 * e), (float)ldexp(ca, f), next - e - f};
+    e = next;
+  }
+}
 
 __device__ __forceinline__ void split(float v, _Float16* hi, _Float16* lo) {
   *hi = (_Float16)v;
@@ -148,12 +190,26 @@ __global__ __launch_bounds__(256) void first_kernel(OrthoArgs a, OrthoLayout l) 
       for (int e = 0; e < 4; ++e) raw[u][e] = r < a.rows && from + e < a.cols ? p[e] : (T)0.f;
     }
   }
+  Scale usual{};  // of the lane's step
+  if (blockIdx.x == 0 && (int)threadIdx.x < a.steps) {
+    const double* k = a.coefficients + 3 * threadIdx.x;
+    usual = Scale{(float)k[1], (float)k[2], (float)k[0], 0};
+  }
   const double* sums = reinterpret_cast<const double*>(ws + l.sums) + (threadIdx.x & 63);
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < kSumParts / 64; ++i) s += sums[i * 64];
   s = wave_sum(s);
-  const double f = (double)kScaleX / (sqrt(s) + a.eps);
+  const double root = sqrt(s), norm = root + a.eps;
+  double f = (double)kScaleX / norm;
+  const bool plain = a.plain && !(root < 100 * a.eps);
+  if (!plain) {
+    const double most = root / norm * 1.001;  // with room for rounding
+    f = ldexp(f, room_above(most));
+    if (blockIdx.x == 0 && threadIdx.x == 0) write_scales(a, most, reinterpret_cast<Scale*>(ws + l.scales));
+  } else if (blockIdx.x == 0 && (int)threadIdx.x < a.steps) {
+    reinterpret_cast<Scale*>(ws + l.scales)[threadIdx.x] = usual;
+  }
   float v[4][4];
 #pragma unroll
   for (int u = 0; u < 4; ++u)
@@ -275,6 +331,17 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
   const uint32_t part = block / step.tiles;
   block -= part * step.tiles;
   char* ws = a.ws + matrix * l.per_matrix;
+  const constant_scales scales = (constant_scales)(ws + l.scales) + step.index;
+  float scale_a = 0.f, scale_b = 0.f, scale_c = 0.f;
+  int raise = 0;
+  if constexpr (KIND == kSquareA) {
+    scale_b = scales->b;
+    scale_c = scales->c;
+  }
+  if constexpr (APPLY) {
+    scale_a = scales->own;
+    raise = scales->out;
+  }
   // tiles of the upper triangle, row by row, or all
   uint32_t tp = 0, tq = block;
   if constexpr (APPLY) {
@@ -390,7 +457,7 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
   float factor[MP];  // of a X
 #pragma unroll
   for (int i = 0; i < MP; ++i) {
-    factor[i] = step.a;
+    factor[i] = scale_a;
     if constexpr (kOwn) factor[i] += reinterpret_cast<const float*>(ws + l.rest)[p + i];
   }
   // A step is two halves of 32 terms: the products of one from one set of
@@ -447,6 +514,13 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
 #pragma unroll
   for (int t = 0; t < kStages; ++t)
     if (begin + t < end) fetch(t, begin + t);
+  arrived(scale_a);
+  arrived(scale_b);
+  arrived(scale_c);
+  // Between steps 2^8 at most either way: with p the larger of |a| and |b s^2 + c s^4|
+  // a step takes the bound on s to p s / 10 at least and 2 p s at most, and f is
+  // log2 1/p but for 30.
+  const float raised = KIND == kApplyB ? __builtin_ldexpf(1.f, raise) : 1.f;
   if (end - begin >= kStages)
     wait_for_loads<(kStages - 1) * kLoads>();
   else
@@ -518,9 +592,9 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
           float was = (float)had[g & 1][r][0][e];
           if constexpr (PARTS == 2) was += (float)had[g & 1][r][1][e];
           if constexpr (KIND == kSquareA)
-            v[i][e] = __builtin_fmaf(step.c, sum * (kScaleB / (kScaleA * kScaleA)), step.b * (was * (kScaleB / kScaleA)));
+            v[i][e] = __builtin_fmaf(scale_c, sum * (kScaleB / (kScaleA * kScaleA)), scale_b * (was * (kScaleB / kScaleA)));
           else
-            v[i][e] = __builtin_fmaf(factor[i], was, sum * (1.f / kScaleB));
+            v[i][e] = __builtin_fmaf(factor[i] * raised, was, sum * (raised / kScaleB));
         }
         if constexpr (KIND == kSquareA && PARTS == 1) {  // what fp16 leaves out of the diagonal
           if (p + i == q + 32 * j + e)
@@ -555,7 +629,7 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
         for (int e = 0; e < 8; ++e) {
           float t[MP];
 #pragma unroll
-          for (int i = 0; i < MP; ++i) t[i] = v[i][e] * f;
+          for (int i = 0; i < MP; ++i) t[i] = __builtin_ldexpf(v[i][e] * f, raise);
           if (c + e < m) store_out(a.out[matrix], a.out_dtype, (c + e) * a.out_stride + p, t, n - p);
         }
       } else {
@@ -563,7 +637,7 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
         for (int i = 0; i < MP; ++i) {
           float t[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = v[i][e] * f;
+          for (int e = 0; e < 8; ++e) t[e] = __builtin_ldexpf(v[i][e] * f, raise);
           if (p + i < n) store_out(a.out[matrix], a.out_dtype, (p + i) * a.out_stride + c, t, m - c);
         }
       }
@@ -671,9 +745,7 @@ template <int PARTS>
 hipError_t steps_of(const OrthoArgs& a, const OrthoLayout& l, int count, hipStream_t st) {
   for (int s = 0; s < a.steps; ++s) {
     OrthoStep step{};
-    step.a = (float)a.coefficients[3 * s];
-    step.b = (float)a.coefficients[3 * s + 1];
-    step.c = (float)a.coefficients[3 * s + 2];
+    step.index = s;
     step.from = s & 1;
     step.parts = l.splits;
     step.part_steps = l.split_steps;
@@ -783,6 +855,7 @@ OrthoLayout layout_of(int64_t n, int64_t m, int parts, int together) {
   }
   l.rest = take((size_t)l.n * 4);
   l.sums = take(kSumParts * 8);
+  l.scales = take(kOrthoSteps * sizeof(Scale));
   l.partials = take(l.splits > 1 ? s * 2 * l.splits : 0);
   l.per_matrix = at;
   l.total = at * l.together;

@@ -1,4 +1,4 @@
-"""Orthogonal updates on the GPU where they are hard: low rank over many steps.
+"""Orthogonal updates on the GPU where they are hard: low rank over many steps, and values far below 1.
 Against the formula in 64 bits; tolerances are counted in roundings."""
 
 import math
@@ -9,7 +9,7 @@ import torch
 import distributed_sgd_gradient_amd as A
 from conftest import flush_print
 from test_layers_gpu import BF16, DTYPES, F16, F32, gen, ids
-from test_more_layers_gpu import plain_orthogonal
+from test_more_layers_gpu import plain_orthogonal, spectrum, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,35 @@ def test_narrow_special_matrices_over_many_steps(gpu):
     x[3, 19, 89] = float("inf")
     got = A.orthogonalize(x, steps=16)
     assert torch.equal(got[[0, 4]], want[[0, 4]]) and not bool(got[1].any()) and bool(got[2:4].isnan().all())
+
+
+@pytest.mark.parametrize("out", DTYPES, ids=ids)
+@pytest.mark.parametrize("n,m", [(65, 66), (300, 400), (512, 512), (130, 900)])
+def test_wide_updates_far_below_eps(gpu, n, m, out):
+    """X keeps its digits however small the update is beside eps; matrices of one
+    call may differ in that.  scale brings the results into out's range."""
+    x = spectrum(620, n, m, F32, "strong", 3)
+    norm = float(x[0].double().norm())
+    x[1] *= 2.0 ** -20
+    for ratio in (0.3, 3.0, 1e2, 1e4, 1e8):
+        eps = norm * ratio
+        got = A.orthogonalize(x, dtype=out, eps=eps, scale=ratio)
+        want = plain_orthogonal(x, eps=eps, scale=ratio)
+        for i in (0, 1, 2):
+            if i == 1 and out == F16:
+                continue  # below fp16's normal numbers
+            far = off(got[i], want[i])
+            flush_print(f"  {n}x{m} to {out}, eps {ratio:g} of the norm, matrix {i}: off by {far:.3g}")
+            assert far <= tolerance(out, max(n, m), 5)
+        assert torch.equal(A.orthogonalize(x[2], dtype=out, eps=eps, scale=ratio),
+                           A.orthogonalize(x[2:], dtype=out, eps=eps, scale=ratio)[0])
+
+
+def test_wide_steps_that_shrink(gpu):
+    x = spectrum(630, 200, 300, F32)
+    for ks in ([(0.01, 0.2, 0.3)] * 3, [(1e-3, 0.0, 0.0)] * 5, [(0.02, 0.0, 0.0), (3.0, -3.2, 1.2)]):
+        got = A.orthogonalize(x, steps=len(ks), coefficients=ks)
+        far = off(got, plain_orthogonal(x, ks))
+        flush_print(f"  shrinking: off by {far:.3g}")
+        assert far <= tolerance(F32, 300, len(ks))
+    assert not bool(A.orthogonalize(x, coefficients=(0.0, 0.0, 0.0)).any())

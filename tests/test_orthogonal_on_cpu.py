@@ -1,6 +1,6 @@
 """Orthogonal updates on the CPU, from their own sources (see
 test_kernels_on_cpu.py), against the definition in long double where it is
-hard: matrices of low rank over many steps."""
+hard: matrices of low rank over many steps, and values far below 1."""
 
 import math
 import subprocess
@@ -54,3 +54,30 @@ def narrow_limit(out, steps, coefficients, rounded):
 def test_narrow_low_rank_over_many_steps(orthogonal, rows, cols, rank, rounded, steps, coefficients, out):
     limit = narrow_limit(out, steps, coefficients, rounded)
     run(orthogonal, rows, cols, F32, out, steps, rank, rounded, 1e-7, limit, *[c for k in coefficients for c in k])
+
+
+@pytest.mark.parametrize("rows,cols,steps,eps,coefficients,value", [
+    (65, 66, 5, 1e2, [DEFAULT], 1),  # beside a norm of some 40
+    (65, 66, 5, 1e4, [DEFAULT], 1),
+    (65, 66, 5, 1e8, [DEFAULT], 1),
+    (65, 66, 5, 1e10, [DEFAULT], 1),
+    (65, 66, 5, 1e25, [DEFAULT], 1),
+    (140, 70, 12, 1e6, [DEFAULT], 1),
+    # steps that shrink every value, or take cubes only; B far below its largest
+    (65, 66, 3, 1e-7, [(0.01, 0.2, 0.3)], 1),
+    (65, 66, 3, 1e5, [(0.01, 0.2, 0.3)], 1),
+    (65, 66, 2, 1e5, [(0.0, 1.0, 0.0)], 3),
+    (65, 66, 3, 1e4, [(0.001, 25.0, -25.0), (0.5, 0.0, 0.0), DEFAULT], 25),
+    (65, 66, 2, 1e4, [(1.0, -31.5, 31.5)], 31.5),
+])
+def test_wide_values_far_below_one(orthogonal, rows, cols, steps, eps, coefficients, value):
+    """A step's operands lose 2^-22 of themselves in two parts, and sums of k
+    terms sqrt(k) roundings, which the coefficients scale; relative to the result
+    whatever its scale is.  (Cubes take three times what X is off by; `value`
+    bounds b and c where they are larger.)"""
+    part = 2.0 ** -22 + math.sqrt(max(rows, cols)) * 2.0 ** -24
+    limit = max(6.81, value) * part * math.sqrt(steps)
+    k = [c for three in coefficients for c in three]
+    run(orthogonal, rows, cols, F32, F32, steps, 0, 0, eps, limit, *k)
+    if value == 1 and eps < 1e5:
+        run(orthogonal, rows, cols, BF16, BF16, steps, 0, 0, eps, math.hypot(limit, 2.0 ** -8 / math.sqrt(3)), *k)
