@@ -868,9 +868,11 @@ OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtyp
   const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
   if (n <= kOrthoNarrow) return ortho_narrow_layout(count, rows, cols);
   const int parts = out_dtype == 2 && n > kOnePartSide ? 1 : 2;
-  const OrthoLayout l = layout_of(n, m, parts, (int)std::min<int64_t>(count, kOrthoWide));
-  if (l.total <= kOrthoWorkspace) return l;
-  return layout_of(n, m, parts, (int)std::max<size_t>(1, kOrthoWorkspace / l.per_matrix));
+  OrthoLayout l = layout_of(n, m, parts, (int)std::min<int64_t>(count, kOrthoWide));
+  // fewer matrices may be padded further, or have A's sums in more parts
+  while (l.total > kOrthoWorkspace && l.together > 1)
+    l = layout_of(n, m, parts, (int)std::max<size_t>(1, std::min<size_t>(l.together - 1, kOrthoWorkspace / l.per_matrix)));
+  return l;
 }
 
 hipError_t launch_ortho(int dtype, const OrthoCall& call, hipStream_t st) {
