@@ -193,6 +193,7 @@ struct OrthoLayout {
   size_t per_matrix, total;
 };
 OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtype);
+size_t ortho_workspace(int64_t count, int64_t rows, int64_t cols, int out_dtype);
 
 // At most what a step makes of singular values s up to `most`, |a s + b s^3 + c
 // s^5|, and what it adds to a, |b s^2 + c s^4|.

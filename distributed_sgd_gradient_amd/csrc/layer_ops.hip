@@ -713,7 +713,7 @@ int check_ortho(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
 
 int64_t orthogonalize_bytes(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
   RETURN_IF(check_ortho(count, rows, cols, out_dtype));
-  return count == 0 || rows == 0 ? 0 : (int64_t)ortho_layout(count, rows, cols, out_dtype).total;
+  return count == 0 || rows == 0 ? 0 : (int64_t)ortho_workspace(count, rows, cols, out_dtype);
 }
 
 // Follows the largest singular value through the steps: the kernels hold X and
@@ -750,7 +750,7 @@ int orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t col
   if (!std::isfinite((float)scale)) return fail(ADASUM_EINVAL, "scale must be finite in fp32");
   if (count == 0 || rows == 0) return ADASUM_OK;
   if (x == nullptr || out == nullptr) return einval("%s is NULL", x == nullptr ? "x" : "out");
-  const size_t need = ortho_layout(count, rows, cols, out_dtype).total;
+  const size_t need = ortho_workspace(count, rows, cols, out_dtype);
   RETURN_IF(check_workspace(workspace, workspace_bytes, need));
   std::vector<Buffer> b;
   std::vector<int> index;

@@ -40,7 +40,11 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <map>
+#include <mutex>
+#include <tuple>
 #include <type_traits>
+#include <vector>
 
 #include "elem.h"
 #include "layer_ops.h"
@@ -873,6 +877,27 @@ OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtyp
   while (l.total > kOrthoWorkspace && l.together > 1)
     l = layout_of(n, m, parts, (int)std::max<size_t>(1, std::min<size_t>(l.together - 1, kOrthoWorkspace / l.per_matrix)));
   return l;
+}
+
+// A call of fewer matrices can take more: its tiles, and so its padding and the
+// parts of A's sums, are others.  A workspace for many is for fewer too, so what
+// `count` need is the most of all calls up to it; kept for each shape, since the 32
+// layouts take some 60 us.
+size_t ortho_workspace(int64_t count, int64_t rows, int64_t cols, int out_dtype) {
+  const int64_t n = std::min(rows, cols), m = std::max(rows, cols);
+  if (n <= kOrthoNarrow) return ortho_narrow_layout(count, rows, cols).total;
+  constexpr size_t kShapes = 1024;
+  static std::mutex mutex;
+  static std::map<std::tuple<int64_t, int64_t, int>, std::vector<size_t>> kept;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (kept.size() >= kShapes) kept.clear();
+  std::vector<size_t>& most = kept[{n, m, out_dtype}];  // of one matrix, of two, ..
+  const size_t together = (size_t)std::min<int64_t>(count, kOrthoWide);
+  while (most.size() < together) {
+    const size_t one = ortho_layout((int64_t)most.size() + 1, rows, cols, out_dtype).total;
+    most.push_back(most.empty() ? one : std::max(one, most.back()));
+  }
+  return most[together - 1];
 }
 
 hipError_t launch_ortho(int dtype, const OrthoCall& call, hipStream_t st) {

@@ -85,7 +85,9 @@ def orthogonalize(update, *, steps=STEPS, coefficients=COEFFICIENTS, eps=1e-7, s
     their rounding), from two for float32 and float16 results (off by less than
     products of fp32 values).
 
-    workspace: as for the layer operators; of a list, what its largest call needs.
+    workspace: as for the layer operators; of a list, what its largest call needs
+    (matrices of one shape and spacing are one call).  What many matrices need is
+    enough for fewer of the same sides.
     """
     single = isinstance(update, torch.Tensor)
     given = [update] if single else list(update)

@@ -468,7 +468,8 @@ ADASUM_API int adasum_relative_bias_grad(const void* dscores, int64_t batch, int
  *                the steps), and |b s^2 + c s^4| below 31 (30).
  *   eps          a positive normal fp32 number.
  *   scale        finite in fp32.
- *   workspace    adasum_orthogonalize_workspace_bytes(...) bytes.
+ *   workspace    adasum_orthogonalize_workspace_bytes(...) bytes, which are enough
+ *                for fewer matrices of these sides too.
  *
  * Operands of the products are fp16, their sums fp32; X itself has 22 bits.
  * bf16 results take one part of each operand (off by some 0.15 % of the norm,

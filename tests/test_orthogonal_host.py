@@ -29,3 +29,13 @@ def test_workspace_of_two_or_more_is_capped():
         dtype = rng.choice([F32, F16, BF16])
         if need(1, rows, cols, dtype) <= CAP:
             assert need(rng.choice([2, 3, 5, 11, 32, 64, 65536]), rows, cols, dtype) <= CAP, (rows, cols, dtype)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(775, 4283, F32), (1024, 4096, F32), (137, 1164, F32), (1024, 1024, BF16),
+                                             (4080, 19521, BF16), (64, 500, F32), (300, 50, F16)])
+def test_a_workspace_for_many_is_for_fewer_too(rows, cols, dtype):
+    many = [need(count, rows, cols, dtype) for count in (*range(1, 131), 1000, 65536)]
+    assert many == sorted(many)
+    # asked for in any order, and of the transpose
+    other = [need(count, cols, rows, dtype) for count in (65536, 1000, *range(130, 0, -1))]
+    assert other == many[::-1]
