@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(BiasGradArgs a, BiasGrad
       }
     }
   }
-  // the groups' sums, added in their order
+  // the groups' sums, added in their order in fp64 and rounded once
   __shared__ float part[256 * VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) part[e * 256 + threadIdx.x] = acc[e];
@@ -200,10 +200,10 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(BiasGradArgs a, BiasGrad
     float* out = a.partials + ((int64_t)split * a.heads + head) * diagonals;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      float s = 0.f;
+      double s = 0.0;
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) s += part[e * 256 + g * LPD + lane];
-      if (d0 + e < diagonals) out[d0 + e] = s;
+      for (int g = 0; g < GROUPS; ++g) s += (double)part[e * 256 + g * LPD + lane];
+      if (d0 + e < diagonals) out[d0 + e] = (float)s;
     }
   }
 }
