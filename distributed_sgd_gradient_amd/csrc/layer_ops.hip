@@ -728,7 +728,7 @@ int check_coefficients(int steps, const double* k, int* plain) {
     if (!std::isfinite((float)a) || !std::isfinite((float)b) || !std::isfinite((float)c))
       return fail(ADASUM_EINVAL, "coefficients must be finite in fp32");
     const OrthoBound bound = ortho_bound(a, b, c, most);
-    if (!(bound.value <= 1.9) || !(bound.added <= 30.0))
+    if (!(bound.value < 2.0) || !(bound.added <= 30.0))
       return fail(ADASUM_EINVAL, "coefficients must keep singular values below 2, and b A + c A^2 below 31");
     if (bound.value <= 0.5) *plain = 0;
     most = std::max(bound.value * 1.01, 1e-3);

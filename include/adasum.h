@@ -464,8 +464,9 @@ ADASUM_API int adasum_relative_bias_grad(const void* dscores, int64_t batch, int
  *                apart.  out[k] may be x[k] (with its stride and type).  Sides
  *                are at most 2^15, count at most 2^16.
  *   coefficients host array: steps (1 to 16) times a, b, c.  Refused unless they
- *                keep singular values of up to 1 below 2 (1.9, followed through
- *                the steps), and |b s^2 + c s^4| below 31 (30).
+ *                keep singular values of up to 1 below 2 (followed through the
+ *                steps, with 1 % of room behind each), and |b s^2 + c s^4| at 30
+ *                at most.
  *   eps          a positive normal fp32 number.
  *   scale        finite in fp32.
  *   workspace    adasum_orthogonalize_workspace_bytes(...) bytes, which are enough

@@ -116,3 +116,26 @@ def test_wide_steps_that_shrink(gpu):
         flush_print(f"  shrinking: off by {far:.3g}")
         assert far <= tolerance(F32, 300, len(ks))
     assert not bool(A.orthogonalize(x, coefficients=(0.0, 0.0, 0.0)).any())
+
+
+@pytest.mark.parametrize("out", DTYPES, ids=ids)
+@pytest.mark.parametrize("n,m", [(40, 90), (120, 200), (300, 500)])
+def test_values_just_below_two(gpu, n, m, out):
+    """The steepest steps that are allowed, on singular values that they take to
+    their peaks.  A step's operands lose a part of themselves, which b and c scale,
+    and the next one scales that by a at most."""
+    ks = [(8.2051604139, -22.9015997, 16.4606545), (4.0663961, -2.8611614, 0.5183957)]
+    s = torch.zeros(n, dtype=torch.float64)
+    s[:12] = torch.tensor([0.86, 0.3, 0.25, 0.2, 0.15, 0.12, 0.1, 0.08, 0.05, 0.03, 0.02, 0.01])
+    left = torch.linalg.qr(torch.randn(n, n, generator=gen(640), dtype=torch.float64))[0]
+    right = torch.linalg.qr(torch.randn(m, n, generator=gen(641), dtype=torch.float64))[0]
+    x = ((left * s) @ right.t().contiguous()).float().cuda()
+    for steps in (1, 2):
+        got = A.orthogonalize(x, steps=steps, coefficients=ks[:steps], dtype=out)
+        want = plain_orthogonal(x, ks[:steps])
+        assert float(torch.linalg.matrix_norm(want, 2)) > 1.8
+        part = 2.0 ** -12 if out == BF16 and n > 256 else 2.0 ** -22 + math.sqrt(m) * 2.0 ** -24
+        limit = 39.4 * part * (1 if steps == 1 else 4.1) + 3.4 * part * (steps - 1) + HALF[out]
+        far = off(got, want)
+        flush_print(f"  {n}x{m} to {out}, {steps} steps: off by {far:.3g}, limit {limit:.3g}")
+        assert far <= limit

@@ -39,3 +39,27 @@ def test_a_workspace_for_many_is_for_fewer_too(rows, cols, dtype):
     # asked for in any order, and of the transpose
     other = [need(count, cols, rows, dtype) for count in (65536, 1000, *range(130, 0, -1))]
     assert other == many[::-1]
+
+
+def refusal(*coefficients):
+    """What an otherwise good call without a workspace, which is looked at last, is refused for."""
+    from test_more_layers_host import CALLS, coefficients as array
+    args = {**CALLS["adasum_orthogonalize"], "steps": len(coefficients), "workspace": None,
+            "coefficients": array(*[c for three in coefficients for c in three])}
+    lib = _native.lib()
+    assert lib.adasum_orthogonalize(*args.values()) == _native.EINVAL
+    return lib.adasum_last_error().decode()
+
+
+# Steep first steps: the largest singular value reaches 1.992, 1.966, 1.866, 1.560, .. at most.
+STEEP = [(8.2051604139, -22.9015997, 16.4606545), (4.0663961, -2.8611614, 0.5183957), (3.9095949, -2.8233675, 0.5250336)]
+
+
+def test_coefficients_below_two_are_allowed():
+    """Values up to 2 are what is stated; 0.1 % of room at the start and 1 % at each
+    step are for rounding."""
+    for k in ([STEEP[0]], STEEP, [(1.99, 0.0, 0.0), (0.95, 0.0, 0.0)], [(-1.99, 0.0, 0.0)]):
+        assert "workspace" in refusal(*k)
+    for k in ([(2.0, 0.0, 0.0)], [(1.99, 0.0, 0.0), (1.0, 0.0, 0.0)], [(1.4, 0.0, 0.0), (1.4, 0.0, 0.0), (1.1, 0.0, 0.0)],
+              [(8.3, -23.3, 17.0)]):
+        assert "below 2" in refusal(*k)
