@@ -663,11 +663,28 @@ int relative_bias_grad(const void* dscores, int64_t batch, int64_t heads, int64_
   return launch(kBias, "relative bias gradient", bytes, st, [&] { return launch_bias_grad(dtype, a, st); });
 }
 
+// One of many buffers: rows of `width` bytes, `pitch` apart.
+struct Rows {
+  Buffer all;
+  size_t width, pitch;
+  int index;  // -1: there is one only
+};
+
+// Whether b, which begins within a's span, has a byte of it.  Rows of one pitch may
+// lie between each other's, as column slices of one matrix do.
+bool share_bytes(const Rows& a, const Rows& b) {
+  if (a.all.bytes == a.width || (b.all.bytes != b.width && a.pitch != b.pitch)) return true;
+  const size_t d = (reinterpret_cast<uintptr_t>(b.all.p) - reinterpret_cast<uintptr_t>(a.all.p)) % a.pitch;
+  return d < a.width || d + b.width > a.pitch;
+}
+
 // The buffers of a call with any number of them, as check_buffers.
-int check_many(const std::vector<Buffer>& given, const std::vector<int>& index) {
+int check_many(const std::vector<Rows>& rows) {
   std::vector<size_t> order;
+  std::vector<Buffer> given;
+  for (const Rows& r : rows) given.push_back(r.all);
   auto name = [&](size_t i) {
-    return std::string(given[i].name) + (index[i] < 0 ? "" : "[" + std::to_string(index[i]) + "]");
+    return std::string(given[i].name) + (rows[i].index < 0 ? "" : "[" + std::to_string(rows[i].index) + "]");
   };
   for (size_t i = 0; i < given.size(); ++i) {
     const Buffer& x = given[i];
@@ -679,17 +696,19 @@ int check_many(const std::vector<Buffer>& given, const std::vector<int>& index) 
   }
   auto start = [&](size_t i) { return reinterpret_cast<uintptr_t>(given[i].p); };
   std::sort(order.begin(), order.end(), [&](size_t i, size_t j) { return start(i) < start(j); });
-  uintptr_t end[2] = {0, 0};  // of what is read, of what is written, up to here
-  size_t by[2] = {0, 0};
+  std::vector<size_t> open[2];  // what is read, what is written, and reaches up to here
   for (size_t i : order) {
-    for (int w = 0; w < 2; ++w)
-      if ((w == 1 || given[i].written) && start(i) < end[w])
-        return einval("%s", (name(i) + " overlaps " + name(by[w])).c_str());
-    const int w = given[i].written ? 1 : 0;
-    if (start(i) + given[i].bytes > end[w]) {
-      end[w] = start(i) + given[i].bytes;
-      by[w] = i;
+    for (int w = given[i].written ? 0 : 1; w < 2; ++w) {
+      size_t left = 0;
+      for (size_t j : open[w]) {
+        if (start(j) + given[j].bytes <= start(i)) continue;
+        if (share_bytes(rows[j], rows[i])) return einval("%s", (name(i) + " overlaps " + name(j)).c_str());
+        open[w][left++] = j;
+      }
+      open[w].resize(left);
     }
+    std::vector<size_t>& mine = open[given[i].written ? 1 : 0];
+    if (mine.empty() || given[mine.back()].p != given[i].p) mine.push_back(i);  // read many times: once
   }
   int device = 0;
   const hipError_t e = hipGetDevice(&device);
@@ -752,17 +771,15 @@ int orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t col
   if (x == nullptr || out == nullptr) return einval("%s is NULL", x == nullptr ? "x" : "out");
   const size_t need = ortho_workspace(count, rows, cols, out_dtype);
   RETURN_IF(check_workspace(workspace, workspace_bytes, need));
-  std::vector<Buffer> b;
-  std::vector<int> index;
+  std::vector<Rows> b;
+  const size_t x_size = size_of(dtype), out_size = size_of(out_dtype);
   for (int64_t i = 0; i < count; ++i) {
     const bool in_place = x[i] == out[i] && x_stride == out_stride && dtype == out_dtype;
-    b.push_back({x[i], in_place ? 0 : x_bytes, size_of(dtype), "x", false});
-    b.push_back({out[i], out_bytes, size_of(out_dtype), "out", true});
-    index.insert(index.end(), {(int)i, (int)i});
+    b.push_back({{x[i], in_place ? 0 : x_bytes, x_size, "x", false}, cols * x_size, x_stride * x_size, (int)i});
+    b.push_back({{out[i], out_bytes, out_size, "out", true}, cols * out_size, out_stride * out_size, (int)i});
   }
-  b.push_back({workspace, need, 16, "workspace", true});
-  index.push_back(-1);
-  RETURN_IF(check_many(b, index));
+  b.push_back({{workspace, need, 16, "workspace", true}, need, need, -1});
+  RETURN_IF(check_many(b));
   OrthoCall call{};
   OrthoArgs& a = call.args;
   a.rows = rows;

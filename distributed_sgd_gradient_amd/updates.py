@@ -44,24 +44,31 @@ def _coefficients(coefficients, steps):
 def _apart(calls, x_size, out_size, workspace):
     """Refuses what only the calls of different shapes together overwrite: a
     matrix that another call writes before it is read, or an output twice.  (A
-    call of its own looks at its own matrices.)"""
-    spans = []
+    call of its own looks at its own matrices.)  Rows of one pitch may lie between
+    each other's, as column slices of one matrix do."""
+    spans = []  # begin, end, written, bytes of a row, of a row and the gap behind it, name
     for (rows, cols, stride, out_stride), (x, y) in calls.items():
-        x_bytes = ((rows - 1) * stride + cols) * x_size
-        out_bytes = ((rows - 1) * out_stride + cols) * out_size
+        sizes = [(((rows - 1) * s + cols) * n, cols * n, s * n) for s, n in ((stride, x_size), (out_stride, out_size))]
         for a, b in zip(x, y):
             if a != b or stride != out_stride or x_size != out_size:  # not in place
-                spans.append((a, a + x_bytes, False, "update"))
-            spans.append((b, b + out_bytes, True, "out"))
+                spans.append((a, a + sizes[0][0], False, *sizes[0][1:], "update"))
+            spans.append((b, b + sizes[1][0], True, *sizes[1][1:], "out"))
     if workspace is not None and _size(workspace):
-        spans.append((workspace.data_ptr(), workspace.data_ptr() + _size(workspace), True, "workspace"))
-    ends = [0, 0]  # of what is read, of what is written, up to here
-    names = ["", ""]
-    for begin, end, written, name in sorted(spans):
-        if begin < ends[1] or written and begin < ends[0]:
-            raise ValueError(f"{name} overlaps {names[1 if begin < ends[1] else 0]} of another matrix")
-        if end > ends[written]:
-            ends[written], names[written] = end, name
+        at, size = workspace.data_ptr(), _size(workspace)
+        spans.append((at, at + size, True, size, size, "workspace"))
+    reaching = ([], [])  # up to here, of what is read, of what is written
+    for span in sorted(spans):
+        begin, end, written, width, pitch, name = span
+        for kind in (0, 1) if written else (1,):
+            reaching[kind][:] = [s for s in reaching[kind] if s[1] > begin]
+            for other in reaching[kind]:
+                at, last, _, row, gap, other_name = other
+                one_row = last - at == row or (end - begin != width and gap != pitch)
+                d = (begin - at) % gap
+                if one_row or d < row or d + width > gap:
+                    raise ValueError(f"{name} overlaps {other_name} of another matrix")
+        if not reaching[written] or reaching[written][-1] != span:  # read many times: once
+            reaching[written].append(span)
 
 
 def orthogonalize(update, *, steps=STEPS, coefficients=COEFFICIENTS, eps=1e-7, scale=1.0, dtype=None, out=None,
@@ -80,10 +87,11 @@ def orthogonalize(update, *, steps=STEPS, coefficients=COEFFICIENTS, eps=1e-7, s
     NaN, one of zeros stays zero.
 
     dtype: of the result (default: update's); out: tensors like the result, which
-    may be the update itself.  Products are formed from fp16 operands: from one
-    part each for bfloat16 results (off by some 0.15 % of the norm, as much as
-    their rounding), from two for float32 and float16 results (off by less than
-    products of fp32 values).
+    may be the update itself.  Matrices may be column slices of one buffer, also
+    where they are written.  Products are formed from fp16 operands: from one part
+    each for bfloat16 results (off by some 0.15 % of the norm, as much as their
+    rounding; for less, ask for float32 and round that), from two for float32 and
+    float16 results (off by less than products of fp32 values).
 
     workspace: as for the layer operators; of a list, what its largest call needs
     (matrices of one shape and spacing are one call).  What many matrices need is

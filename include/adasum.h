@@ -461,8 +461,10 @@ ADASUM_API int adasum_relative_bias_grad(const void* dscores, int64_t batch, int
  *
  *   x, out       host arrays of count pointers to matrices of rows x cols
  *                elements of dtype and out_dtype, rows x_stride and out_stride
- *                apart.  out[k] may be x[k] (with its stride and type).  Sides
- *                are at most 2^15, count at most 2^16.
+ *                apart.  out[k] may be x[k] (with its stride and type), and
+ *                matrices of one stride in bytes may lie between each other's
+ *                rows, as column slices of one matrix do.  Sides are at most
+ *                2^15, count at most 2^16.
  *   coefficients host array: steps (1 to 16) times a, b, c.  Refused unless they
  *                keep singular values of up to 1 below 2 (followed through the
  *                steps, with 1 % of room behind each), and |b s^2 + c s^4| at 30

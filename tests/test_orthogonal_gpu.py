@@ -139,3 +139,39 @@ def test_values_just_below_two(gpu, n, m, out):
         far = off(got, want)
         flush_print(f"  {n}x{m} to {out}, {steps} steps: off by {far:.3g}, limit {limit:.3g}")
         assert far <= limit
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("rows,widths", [(96, (70, 70, 70)), (30, (70, 70, 70)), (200, (131, 33, 33)), (300, (64, 300, 7)),
+                                         (1, (5, 9, 5))])
+def test_column_slices_of_one_buffer(gpu, rows, widths, dtype):
+    """A fused weight's parts, in place and as outputs: the bits of matrices that lie
+    apart, and every other column as it was."""
+    flush_print(f"slices {rows} x {widths} {dtype}")
+    wide = spectrum(650, rows, sum(widths) + 6, dtype)
+    firsts = [3 + sum(widths[:i]) for i in range(len(widths))]
+    parts = [wide[:, a:a + w] for a, w in zip(firsts, widths)]
+    want = [A.orthogonalize(p.contiguous()) for p in parts]
+    buffer = torch.full_like(wide, 7.0)
+    outs = [buffer[:, a:a + w] for a, w in zip(firsts, widths)]
+    before = wide.clone()
+    for _ in range(3):
+        got = A.orthogonalize(parts, out=outs)
+        assert all(torch.equal(g, w) for g, w in zip(got, want)) and torch.equal(wide, before)
+        assert bool((buffer[:, :3] == 7).all()) and bool((buffer[:, -3:] == 7).all())
+        wide.copy_(before)
+        A.orthogonalize(parts, out=parts)
+        assert all(torch.equal(p, w) for p, w in zip(parts, want))
+        assert torch.equal(wide[:, :3], before[:, :3]) and torch.equal(wide[:, -3:], before[:, -3:])
+        wide.copy_(before)
+    with pytest.raises((ValueError, A.AdasumError), match="overlaps"):
+        A.orthogonalize(parts, out=[outs[0], outs[1], buffer[:, firsts[2] - 1:firsts[2] - 1 + widths[2]]])
+
+
+def test_many_column_slices(gpu):
+    """One view of all heads: [heads, rows, columns] of a [rows, heads * columns]."""
+    wide = spectrum(651, 128, 64 * 40, BF16)
+    heads = wide.view(128, 40, 64).transpose(0, 1)
+    want = A.orthogonalize(heads.contiguous())
+    assert torch.equal(A.orthogonalize(heads), want)
+    assert A.orthogonalize(heads, out=heads) is heads and torch.equal(heads, want)
