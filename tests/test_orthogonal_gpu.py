@@ -175,3 +175,24 @@ def test_many_column_slices(gpu):
     want = A.orthogonalize(heads.contiguous())
     assert torch.equal(A.orthogonalize(heads), want)
     assert A.orthogonalize(heads, out=heads) is heads and torch.equal(heads, want)
+
+
+@pytest.mark.parametrize("n,m,dtype,kind", [
+    (8192, 300, F32, "strong"), (300, 8192, F32, "rank"), (300, 8192, BF16, "strong"), (32768, 70, F32, "strong"),
+    (32768, 64, F32, "strong"), (7, 32768, BF16, "normal"), (4500, 4300, F32, "strong"), (4300, 4500, F16, "normal"),
+    (6000, 5000, BF16, "strong"), (1025, 9000, F32, "normal"),
+])
+def test_great_sides(gpu, n, m, dtype, kind):
+    """Sides above 4096.  Of a matrix of rank 3, rounded to fp32, what that rounding
+    adds, 2^-24 of the norm, is raised by 3.4445^5 = 485 here and in the reference;
+    the parts' 2^-22 likewise."""
+    flush_print(f"great sides {n}x{m} {dtype} {kind}")
+    x = spectrum(660, n, m, dtype, kind)
+    got = A.orthogonalize(x)
+    far = off(got, plain_orthogonal(x))
+    limit = tolerance(dtype, max(n, m), 5)
+    if kind == "rank":
+        limit += 485 * 2.0 ** -22
+    flush_print(f"  off by {far:.3g}, limit {limit:.3g}")
+    assert far <= limit
+    assert torch.equal(A.orthogonalize(x), got)
