@@ -112,9 +112,18 @@ __device__ __forceinline__ int room_above(double s) {
   return -k;
 }
 
-// The powers of all steps for an X whose singular values are at most `most`.
-__device__ void write_scales(const OrthoArgs& a, double most, Scale* to) {
-  int e = room_above(most);
+// The first e, from the exponents alone: norm / (norm + eps) is below 2^-e.
+__device__ __forceinline__ int first_room(const OrthoArgs& a, double norm) {
+  int of_norm, of_sum;
+  frexp(norm, &of_norm);
+  frexp(norm + a.eps, &of_sum);
+  return max(0, of_sum - of_norm - 1);
+}
+
+// The powers of all steps.
+__device__ void write_scales(const OrthoArgs& a, double norm, Scale* to) {
+  int e = first_room(a, norm);
+  double most = norm / (norm + a.eps) * 1.001;  // that a singular value is, with room for rounding
   for (int s = 0; s < a.steps; ++s) {
     const double ca = a.coefficients[3 * s], cb = a.coefficients[3 * s + 1], cc = a.coefficients[3 * s + 2];
     const OrthoBound bound = ortho_bound(ca, cb, cc, most);
@@ -167,12 +176,35 @@ __global__ __launch_bounds__(256) void square_sum_kernel(OrthoArgs a, OrthoLayou
   if (threadIdx.x == 0) reinterpret_cast<double*>(a.ws + blockIdx.y * l.per_matrix + l.sums)[blockIdx.x] = sums[0];
 }
 
+// The norm, from its parts, in every lane.
+__device__ __forceinline__ double norm_of(const char* ws, const OrthoLayout& l) {
+  const double* sums = reinterpret_cast<const double*>(ws + l.sums) + (threadIdx.x & 63);
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kSumParts / 64; ++i) s += sums[i * 64];
+  return sqrt(wave_sum(s));
+}
+// All powers are 1 (also of a norm that is NaN).
+__device__ __forceinline__ bool usual(const OrthoArgs& a, double norm) { return a.plain && !(norm < 100 * a.eps); }
+
 // X, 64 x 64 values a workgroup: a vector of four values of each of four rows a
-// lane, turned in LDS where the matrix is tall.
+// lane, turned in LDS where the matrix is tall.  The last workgroup of a matrix
+// leaves the steps' powers.
 template <typename T>
 __global__ __launch_bounds__(256) void first_kernel(OrthoArgs a, OrthoLayout l) {
   __shared__ float tile[64][65];
   char* ws = a.ws + blockIdx.y * l.per_matrix;
+  if (blockIdx.x == gridDim.x - 1) {
+    Scale* const scales = reinterpret_cast<Scale*>(ws + l.scales);
+    const double norm = norm_of(ws, l);
+    if (!usual(a, norm)) {
+      if (threadIdx.x == 0) write_scales(a, norm, scales);
+    } else if ((int)threadIdx.x < a.steps) {
+      const double* k = a.coefficients + 3 * threadIdx.x;
+      scales[threadIdx.x] = Scale{(float)k[1], (float)k[2], (float)k[0], 0};
+    }
+    return;
+  }
   const uint32_t tiles_m = (uint32_t)(l.m / 64), ti = blockIdx.x / tiles_m, tk = blockIdx.x - ti * tiles_m;
   const int64_t i0 = (int64_t)ti * 64, k0 = (int64_t)tk * 64;
   const T* x = static_cast<const T*>(a.x[blockIdx.y]);
@@ -194,26 +226,8 @@ __global__ __launch_bounds__(256) void first_kernel(OrthoArgs a, OrthoLayout l) 
       for (int e = 0; e < 4; ++e) raw[u][e] = r < a.rows && from + e < a.cols ? p[e] : (T)0.f;
     }
   }
-  Scale usual{};  // of the lane's step
-  if (blockIdx.x == 0 && (int)threadIdx.x < a.steps) {
-    const double* k = a.coefficients + 3 * threadIdx.x;
-    usual = Scale{(float)k[1], (float)k[2], (float)k[0], 0};
-  }
-  const double* sums = reinterpret_cast<const double*>(ws + l.sums) + (threadIdx.x & 63);
-  double s = 0.0;
-#pragma unroll
-  for (int i = 0; i < kSumParts / 64; ++i) s += sums[i * 64];
-  s = wave_sum(s);
-  const double root = sqrt(s), norm = root + a.eps;
-  double f = (double)kScaleX / norm;
-  const bool plain = a.plain && !(root < 100 * a.eps);
-  if (!plain) {
-    const double most = root / norm * 1.001;  // with room for rounding
-    f = ldexp(f, room_above(most));
-    if (blockIdx.x == 0 && threadIdx.x == 0) write_scales(a, most, reinterpret_cast<Scale*>(ws + l.scales));
-  } else if (blockIdx.x == 0 && (int)threadIdx.x < a.steps) {
-    reinterpret_cast<Scale*>(ws + l.scales)[threadIdx.x] = usual;
-  }
+  const double norm = norm_of(ws, l);
+  const double f = ldexp((double)kScaleX / (norm + a.eps), first_room(a, norm));
   float v[4][4];
 #pragma unroll
   for (int u = 0; u < 4; ++u)
@@ -523,8 +537,8 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
   arrived(scale_c);
   // Between steps 2^8 at most either way: with p the larger of |a| and |b s^2 + c s^4|
   // a step takes the bound on s to p s / 10 at least and 2 p s at most, and f is
-  // log2 1/p but for 30.
-  const float raised = KIND == kApplyB ? __builtin_ldexpf(1.f, raise) : 1.f;
+  // log2 1/p but for 30.  Behind the last as low as the result is, in two factors.
+  const float raised = APPLY ? __builtin_ldexpf(1.f, max(raise, -100)) : 1.f;
   if (end - begin >= kStages)
     wait_for_loads<(kStages - 1) * kLoads>();
   else
@@ -627,13 +641,13 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
     // all MP rows of these columns are there
     if constexpr (KIND == kLastB) {
       const int64_t n = min(a.rows, a.cols), m = max(a.rows, a.cols), c = q + 32 * j;
-      const float f = a.scale * (1.f / kScaleX);
+      const float f = __builtin_ldexpf(a.scale * (1.f / kScaleX), min(raise + 100, 0));
       if (turn) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float t[MP];
 #pragma unroll
-          for (int i = 0; i < MP; ++i) t[i] = __builtin_ldexpf(v[i][e] * f, raise);
+          for (int i = 0; i < MP; ++i) t[i] = v[i][e] * f;
           if (c + e < m) store_out(a.out[matrix], a.out_dtype, (c + e) * a.out_stride + p, t, n - p);
         }
       } else {
@@ -641,7 +655,7 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
         for (int i = 0; i < MP; ++i) {
           float t[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = __builtin_ldexpf(v[i][e] * f, raise);
+          for (int e = 0; e < 8; ++e) t[e] = v[i][e] * f;
           if (p + i < n) store_out(a.out[matrix], a.out_dtype, (p + i) * a.out_stride + c, t, m - c);
         }
       }
@@ -916,7 +930,7 @@ hipError_t launch_ortho(int dtype, const OrthoCall& call, hipStream_t st) {
       e = with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         square_sum_kernel<T><<<dim3(kSumParts, count), 256, 0, st>>>(a, l);
-        first_kernel<T><<<dim3((unsigned)(l.n / 64 * (l.m / 64)), count), 256, 0, st>>>(a, l);
+        first_kernel<T><<<dim3((unsigned)(l.n / 64 * (l.m / 64) + 1), count), 256, 0, st>>>(a, l);
         return hipGetLastError();
       });
       if (e == hipSuccess) e = l.parts == 1 ? steps_of<1>(a, l, count, st) : steps_of<2>(a, l, count, st);
