@@ -6,11 +6,11 @@
 //
 // which takes every singular value s to a s + b s^3 + c s^5.
 //
-// Bound by the matrix cores, the card's power, and X's traffic: 24 matrices of
-// 1024 x 1024 in bf16 take 820 to 850 us, 620 TFLOP/s with half of the symmetric
-// products (a library product of 8192^3 in fp16 reaches 1127).  A step there is 41
-// us of A, 42 of B and 96 of X.  The loops alone take 28, 25 and 70 (1.1, 1.3 and
-// 0.74 PFLOP/s); in A and B the results are written when the loops of all
+// Bound by the matrix cores and X's traffic: 24 matrices of 1024 x 1024 in bf16
+// take 820 to 850 us, 620 TFLOP/s with half of the symmetric products (a library
+// product of 8192^3 in fp16 reaches 1127).  A step there is 41 us of A, 42 of B and
+// 96 of X.  The loops alone take 28, 25 and 70 (1.1, 1.3 and 0.74 PFLOP/s, A's and
+// B's what a library product reaches); in A and B the results are written when the loops of all
 // workgroups have ended, in X beside loads, which wait for them (with the loads of
 // the first steps only X takes 69 too).  Matrices with a side of at most 64 are in
 // orthogonal_narrow.hip.
@@ -21,8 +21,9 @@
 // the steps then raise as if it were signal (a matrix of rank 8: 4e-2 of the
 // result's norm; with hi + lo 4e-4).  What an operand of a product loses is
 // scaled down by the product.  Of bf16 results (PARTS 1) the products take the
-// hi parts only: off by 1.4e-3 of the norm for normally distributed matrices,
-// where the rounding of the result itself costs 1.7e-3.  B's diagonal, its
+// hi parts only: off by 1.1e-3 of the norm for normally distributed matrices of
+// 1024 x 1024 in 5 steps, 3.4e-3 in 12, where the rounding of the result itself
+// costs 1.7e-3.  B's diagonal, its
 // largest values, is kept in fp32 beside its fp16 copy (without: 1.7e-3).
 // fp16 and fp32 results (PARTS 2) take hi hi + hi lo + lo hi: off by less than
 // products in fp32 are.

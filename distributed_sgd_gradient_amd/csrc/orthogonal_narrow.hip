@@ -8,15 +8,16 @@
 //
 // All of these commute and are symmetric, so half of their tiles are computed.
 // G holds the squares of the singular values, so everything is in fp64, and after
-// as many steps as raise what G's rounding is above 2^-20 (8 by default) G is formed
-// again, from Q X0: small singular values have grown by then, and where X has none
-// G is zero again.  Three launches instead of three a step: partial sums of G over
-// the long side, the steps in one workgroup a matrix on the fp64 matrix cores, a
-// wave for each tile of 16 x 16 on and above the diagonal, and the product with X0.  Bound by the latency of the
-// steps, in which three products follow one another: 61 x 769 fp32 in 5 steps
-// takes 8 + 39 + 11 us (the steps with a product's sum in one chain of matrix
-// instructions, and LDS read between them: 48; with fp32 steps through the
-// products of orthogonal.hip: 254 a call against 59).
+// as many steps as raise G's rounding to 2^-20 (8 by default) G is formed again,
+// from Q X0: small singular values have grown by then, and where X has none G is
+// zero again.  Three launches instead of three a step, and two more each time G is
+// formed again: partial sums of G over the long side, the steps in one workgroup a
+// matrix on the fp64 matrix cores, a wave for each tile of 16 x 16 on and above the
+// diagonal, and the product with X0.  Bound by the latency of the steps, in which
+// three products follow one another: 61 x 769 fp32 in 5 steps takes 9 + 40 + 11 us
+// (the steps with a product's sum in one chain of matrix instructions, and LDS read
+// between them: 48; with fp32 steps through the products of orthogonal.hip: 254 a
+// call against 61); 8 steps 82 us a call, 9 steps, with G formed again, 113.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

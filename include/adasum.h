@@ -474,10 +474,11 @@ ADASUM_API int adasum_relative_bias_grad(const void* dscores, int64_t batch, int
  *   workspace    adasum_orthogonalize_workspace_bytes(...) bytes, which are enough
  *                for fewer matrices of these sides too.
  *
- * Operands of the products are fp16, their sums fp32; X itself has 22 bits.
- * bf16 results take one part of each operand (off by some 0.15 % of the norm,
- * as much as their rounding), fp32 and fp16 results two (off by less than
- * products of fp32 values).
+ * Operands of the products are fp16, their sums fp32; X itself has 22 bits,
+ * however small the matrix is beside eps.  bf16 results take one part of each
+ * operand (in 5 steps off by some 0.15 % of the norm, as much as their rounding,
+ * in 12 by 0.35 %), fp32 and fp16 results two (off by less than products of fp32
+ * values).  Where a side is at most 64 everything is fp64.
  */
 ADASUM_API int64_t adasum_orthogonalize_workspace_bytes(int64_t count, int64_t rows, int64_t cols, int out_dtype);
 ADASUM_API int adasum_orthogonalize(const void* const* x, int64_t count, int64_t rows, int64_t cols, int64_t x_stride,
