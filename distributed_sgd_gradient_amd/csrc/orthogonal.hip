@@ -10,10 +10,10 @@
 // take 820 to 850 us, 620 TFLOP/s with half of the symmetric products (a library
 // product of 8192^3 in fp16 reaches 1127).  A step there is 41 us of A, 42 of B and
 // 96 of X.  The loops alone take 28, 25 and 70 (1.1, 1.3 and 0.74 PFLOP/s, A's and
-// B's what a library product reaches); in A and B the results are written when the loops of all
-// workgroups have ended, in X beside loads, which wait for them (with the loads of
-// the first steps only X takes 69 too).  Matrices with a side of at most 64 are in
-// orthogonal_narrow.hip.
+// B's what a library product reaches); in A and B the results are written when the
+// loops of all workgroups have ended, in X beside loads, which wait for them (with
+// the loads of the first steps only X takes 69 too).  Matrices with a side of at
+// most 64 are in orthogonal_narrow.hip.
 //
 // Products take fp16 operands and sum in fp32.  X is kept as hi + lo, two fp16
 // of 22 bits together, and a X is added in fp32 from both: rounding X itself to
@@ -23,10 +23,9 @@
 // scaled down by the product.  Of bf16 results (PARTS 1) the products take the
 // hi parts only: off by 1.1e-3 of the norm for normally distributed matrices of
 // 1024 x 1024 in 5 steps, 3.4e-3 in 12, where the rounding of the result itself
-// costs 1.7e-3.  B's diagonal, its
-// largest values, is kept in fp32 beside its fp16 copy (without: 1.7e-3).
-// fp16 and fp32 results (PARTS 2) take hi hi + hi lo + lo hi: off by less than
-// products in fp32 are.
+// costs 1.7e-3.  B's diagonal, its largest values, is kept in fp32 beside its fp16
+// copy (without it the error grows by a fifth).  fp16 and fp32 results (PARTS 2)
+// take hi hi + hi lo + lo hi: off by less than products in fp32 are.
 //
 // Values are scaled by powers of two so that neither part leaves fp16's normal
 // range: the host admits coefficients only that keep singular values below 2
@@ -611,7 +610,8 @@ __global__ __launch_bounds__((threads_of<T, PARTS>), 2) void product_kernel(Orth
           float was = (float)had[g & 1][r][0][e];
           if constexpr (PARTS == 2) was += (float)had[g & 1][r][1][e];
           if constexpr (KIND == kSquareA)
-            v[i][e] = __builtin_fmaf(scale_c, sum * (kScaleB / (kScaleA * kScaleA)), scale_b * (was * (kScaleB / kScaleA)));
+            v[i][e] = __builtin_fmaf(scale_c, sum * (kScaleB / (kScaleA * kScaleA)),
+                                     scale_b * (was * (kScaleB / kScaleA)));
           else
             v[i][e] = __builtin_fmaf(factor[i] * raised, was, sum * (raised / kScaleB));
         }
@@ -890,7 +890,8 @@ OrthoLayout ortho_layout(int64_t count, int64_t rows, int64_t cols, int out_dtyp
   OrthoLayout l = layout_of(n, m, parts, (int)std::min<int64_t>(count, kOrthoWide));
   // fewer matrices may be padded further, or have A's sums in more parts
   while (l.total > kOrthoWorkspace && l.together > 1)
-    l = layout_of(n, m, parts, (int)std::max<size_t>(1, std::min<size_t>(l.together - 1, kOrthoWorkspace / l.per_matrix)));
+    l = layout_of(n, m, parts,
+                  (int)std::max<size_t>(1, std::min<size_t>(l.together - 1, kOrthoWorkspace / l.per_matrix)));
   return l;
 }
 
