@@ -2,6 +2,7 @@
 Against the formula in 64 bits; tolerances are counted in roundings."""
 
 import math
+import random
 
 import pytest
 import torch
@@ -196,3 +197,32 @@ def test_great_sides(gpu, n, m, dtype, kind):
     flush_print(f"  off by {far:.3g}, limit {limit:.3g}")
     assert far <= limit
     assert torch.equal(A.orthogonalize(x), got)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_anything_allowed(gpu, seed):
+    """Random sides, counts, types, strides, steps, eps and places against the formula."""
+    rng = random.Random(seed)
+    n, m = (int(2 ** rng.uniform(0, 9)) for _ in range(2))
+    if seed % 3 == 0:
+        n = rng.choice([1, 15, 16, 17, 33, 48, 63, 64, 65, 127, 128, 129, 257])
+    count, steps = rng.choice([1, 2, 5, 33, 130]) if n * m < 20000 else rng.choice([1, 3]), rng.randint(1, 8)
+    dtype, out = rng.choice(DTYPES), rng.choice(DTYPES)
+    x = spectrum(700 + seed, n, m, F32, "strong" if min(n, m) > 3 else "normal", count) * 1000
+    ratio = rng.choice([1e-8, 0.2, 1.0, 30.0, 3e3])  # eps beside the norm
+    eps, scale = ratio * float(x[0].double().norm()), max(1.0, ratio) * rng.uniform(0.5, 2.0)
+    scale = float(torch.tensor(scale).float())
+    x = x.to(dtype)
+    flush_print(f"{count}x{n}x{m} {dtype} to {out}, {steps} steps, eps {ratio:g} of the norm")
+    wide = torch.full((count, n + 2, m + rng.randint(0, 5)), float("nan"), dtype=dtype, device="cuda")
+    view = wide[:, 1:n + 1, :m]
+    view.copy_(x)
+    got = A.orthogonalize(view, steps=steps, eps=eps, scale=scale, dtype=out)
+    want = plain_orthogonal(x, [DEFAULT] * steps, eps, scale)
+    limit = tolerance(out, max(n, m), steps)
+    far = off(got, want)
+    flush_print(f"  off by {far:.3g}, limit {limit:.3g}")
+    assert far <= limit
+    if out == dtype:
+        assert A.orthogonalize(view, steps=steps, eps=eps, scale=scale, out=view) is view and torch.equal(view, got)
+        assert bool(wide[:, 0].isnan().all()) and bool(wide[:, -1].isnan().all()) and bool(wide[:, :, m:].isnan().all())
